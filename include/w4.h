@@ -370,6 +370,133 @@ int i8_embed_kmajor(const int64_t *tokens, int64_t T, const int8_t *Qt, int64_t 
                     const float *hs, int64_t K, int64_t N, float *out,
                     int *d_status, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged key-value cache of one layer, between the QKV matmul and the
+ * out-projection of a decode step (pages "zero-tvm": a paged KV cache, its
+ * append and the attention over a page table, an int8 form).
+ *   k, v      [pages, heads, page_size, head_dim] of the type `dtype`
+ *   k_scale,  fp32 [pages, heads, page_size], KV_I8 only (else NULL): the row
+ *   v_scale   stands for code * scale
+ *   weight    fp32 [pages, heads, page_size], may be NULL: the attention weight
+ *             that each position has taken so far
+ *   table     int32 [seqs, cols]: position t of sequence b is slot
+ *             t % page_size of page table[b, t / page_size]
+ * page_size is a power of two from 16 to 4096; head_dim a multiple of 8 from 8
+ * to 256; seqs * cols and every array below 2^40 elements (pools may pass
+ * 2^31: their offsets are 64-bit).  k, v 16-byte aligned, all else 4-byte.
+ * Lengths, positions and page ids are int32 on the device, where the host
+ * cannot check them: a length past cols * page_size (or the call's max_len) or
+ * below 0 is cut to that range, a position or row whose page id lies outside
+ * [0, pages) is left out (not read, not written, no attention), and in each
+ * case d_status (may be NULL) is set to W4_ERR_BAD_SHAPE.  Only the table
+ * entries that a length needs are read; the others may hold anything, and so
+ * may the slots of a page past the length.                                 */
+#define KV_F32 0
+#define KV_F16 1
+#define KV_BF16 2
+#define KV_I8 3
+
+typedef struct kv_cache {
+    void *k;
+    void *v;
+    float *k_scale;
+    float *v_scale;
+    float *weight;
+    int64_t pages;
+    int64_t heads;
+    int64_t page_size;
+    int64_t head_dim;
+    int32_t dtype;
+} kv_cache;
+
+/* Append: row r of k, v (fp32, [rows, heads, head_dim] with the given distance
+ * in floats between rows, at least heads * head_dim: columns of a fused QKV
+ * product fit) is stored at position at[r] of sequence seq[r].  Rounding to
+ * nearest even; KV_I8 stores s = max|x| / 127 (correctly rounded) and
+ * clamp(rint(x / s), -127, 127), a zero row s = 0 and zeros.  weight, if
+ * given, becomes 0 there.  A row with seq[r] < 0 is skipped (padding).  Two
+ * rows at one position, or a page that two sequences of the call both write,
+ * is the caller's race.  A non-finite value is stored as it is (KV_I8: its row
+ * is unspecified and d_status set to W4_ERR_NONFINITE).  No workspace.      */
+int kv_append(const kv_cache *cache, const float *k, int64_t k_stride, const float *v,
+              int64_t v_stride, int64_t rows, const int32_t *table, int64_t seqs, int64_t cols,
+              const int32_t *seq, const int32_t *at, int *d_status, void *stream);
+
+/* Attention of one new token in each sequence over its cached positions
+ * t in [starts[b], lens[b]) (starts may be NULL: from 0):
+ *   s[h, t] = scale * sum_d q[b, h, d] k[b, h / G, t, d],  G = q_heads / heads,
+ *   p[h, :] = softmax over t of s[h, :],  out[b, h, :] = sum_t p[h, t] v[b, h / G, t, :]
+ * q fp32 [seqs, q_heads, head_dim] with q_stride floats between sequences, out
+ * fp32 [seqs, q_heads, head_dim].  q_heads is a multiple of heads.  An empty
+ * range gives zeros.  If cache->weight is given, each attended position's
+ * weight grows by the sum of p[h, t] over the G query heads of its key head; a
+ * page whose weights grow must then belong to one sequence only.
+ * fp32 arithmetic on the values that the cache's type holds, softmax
+ * statistics and sums in fp32; deterministic.  Attended values must be finite:
+ * others make their head's outputs NaN or infinite.  max_len bounds lens for the
+ * launch (0: cols * page_size); lens may be smaller by any amount.  The
+ * workspace (kv_attend_workspace_bytes, 256-byte aligned, any contents, not
+ * shared with a call in flight on another stream) holds the parts that the
+ * length is split into.                                                    */
+size_t kv_attend_workspace_bytes(const kv_cache *cache, int64_t seqs, int64_t q_heads,
+                                 int64_t max_len);
+
+int kv_check_attend_args(const kv_cache *cache, const float *q, int64_t q_stride,
+                         int64_t q_heads, const int32_t *table, int64_t seqs, int64_t cols,
+                         const int32_t *lens, const int32_t *starts, int64_t max_len,
+                         const float *out, const void *workspace, size_t workspace_bytes,
+                         const int *d_status);
+
+int kv_attend(const kv_cache *cache, const float *q, int64_t q_stride, int64_t q_heads,
+              const int32_t *table, int64_t seqs, int64_t cols, const int32_t *lens,
+              const int32_t *starts, int64_t max_len, float scale, float *out, void *workspace,
+              size_t workspace_bytes, int *d_status, void *stream);
+
+/* Eviction by accumulated attention weight (cache->weight, required).  For each
+ * sequence and head on its own, L = lens[b]: if L > keep, the newest
+ * r = min(recent, keep) positions stay, and of the L - r others the keep - r of
+ * largest weight (ties: the lower position; NaN counts as lowest); if
+ * L <= keep every position stays.  The rows that stay (k, v, scales, weight)
+ * are copied in their order to positions 0, 1, .. of the pages of table_out
+ * (int32 [seqs, cols_out], cols_out * page_size >= min(keep, max_len)), which must be
+ * none of the pages read: the old pages, which other sequences may share, are
+ * left as they are.  kept int32 [seqs, heads, keep]: the old positions, ascending,
+ * then -1; lens_out int32 [seqs] = min(L, keep).  keep >= 1, recent >= 0.
+ * max_len as in kv_attend; lengths below 2^24.  No workspace.               */
+int kv_evict(const kv_cache *cache, const int32_t *table, int64_t seqs, int64_t cols,
+             const int32_t *lens, int64_t max_len, int64_t keep, int64_t recent,
+             const int32_t *table_out, int64_t cols_out, int32_t *kept, int32_t *lens_out,
+             int *d_status, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Log probabilities read off the head's logits: x = row m of logits (fp32
+ * [M, N], ld >= N floats between rows), L = log sum_n e^x[n]:
+ *   logprob[m] = x[tokens[m]] - L           (tokens int64 [M], NULL: not wanted)
+ *   entropy[m] = -sum_n e^(x[n]-L) (x[n]-L) (NULL: not wanted)
+ *   top_ids[m, j] int64, top_logprob[m, j] = x[id] - L for the `top` largest, in
+ *   descending order, ties by the lower id  (both NULL if top == 0)
+ * 0 <= top <= 64, top <= N; N >= 1 where M > 0, N < 2^31.  An entry of
+ * -infinity is a forbidden token: probability 0.  A row of nothing else gives
+ * log probabilities of -infinity and entropy 0.  A row with NaN or +infinity gives
+ * NaN, ids -1, and W4_ERR_NONFINITE in d_status; a token outside [0, N) gives NaN
+ * and W4_ERR_BAD_SHAPE.  fp32 sums on values relative to the row's maximum;
+ * deterministic.  Workspace: lp_logprobs_workspace_bytes, 256-byte aligned, any
+ * contents (0: none).                                                      */
+#define LP_MAX_TOP 64
+
+size_t lp_logprobs_workspace_bytes(int64_t M, int64_t N, int64_t top);
+
+int lp_check_logprobs_args(const float *logits, int64_t M, int64_t N, int64_t ld,
+                           const int64_t *tokens, int64_t top, const float *logprob,
+                           const float *entropy, const int64_t *top_ids,
+                           const float *top_logprob, const void *workspace,
+                           size_t workspace_bytes, const int *d_status);
+
+int lp_logprobs(const float *logits, int64_t M, int64_t N, int64_t ld, const int64_t *tokens,
+                int64_t top, float *logprob, float *entropy, int64_t *top_ids,
+                float *top_logprob, void *workspace, size_t workspace_bytes, int *d_status,
+                void *stream);
+
 /* ---- measurement: streaming-read reference ---------------------------------
  * Reads [src, src + bytes) once with 16-byte streaming loads, loads_per_lane
  * (4, 6, 8, 12 or 16) of them per lane, 256 lanes (4 waves) per workgroup,

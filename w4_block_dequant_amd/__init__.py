@@ -14,6 +14,10 @@ functions carry the C names:
     i8_quantize_head(E, ldq)               -> (Q, hs)
     i8_head_logits(x_last, Q, hs)          -> logits
     i8_embed(tokens, Q, hs)                -> rows of the dequantized table
+    kv_append(k, v, K, V, table, seq, at)                  new rows into a paged cache
+    kv_attend(q, K, V, table, lens)        -> out          attention of one new token
+    kv_evict(K, V, weight, table, lens, keep, recent, table_out) -> (kept, lens_out)
+    lp_logprobs(logits, tokens, top)       -> (logprob, entropy, top_ids, top_logprob)
 
 If the library has not been built this module raises ImportError: there is
 no fallback path.
@@ -35,6 +39,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 _P, _I64, _SZ, _INT = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+_FLT = ctypes.c_float
 _SIGS = {
     "w4_abi_version": (_INT, []),
     "w4_strerror": (ctypes.c_char_p, [_INT]),
@@ -76,6 +81,17 @@ _SIGS = {
                                    _P]),
     "i8_check_head_logits_rows_args": (_INT, [_P, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _SZ]),
     "i8_head_logits_rows": (_INT, [_P, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _SZ, _P]),
+    "kv_append": (_INT, [_P, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _P]),
+    "kv_attend_workspace_bytes": (_SZ, [_P, _I64, _I64, _I64]),
+    "kv_check_attend_args": (_INT, [_P, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _P, _SZ,
+                                    _P]),
+    "kv_attend": (_INT, [_P, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _FLT, _P, _P, _SZ, _P,
+                         _P]),
+    "kv_evict": (_INT, [_P, _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P]),
+    "lp_logprobs_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "lp_check_logprobs_args": (_INT, [_P, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _SZ,
+                                      _P]),
+    "lp_logprobs": (_INT, [_P, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _SZ, _P, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -589,3 +605,200 @@ def w4g_matmul_kmajor(x: torch.Tensor, Pq: torch.Tensor, Ps: torch.Tensor, Pm: t
         _ptr(x), M, K, _ptr(Pq), _ptr(Ps), _ptr(Pm), N, _ptr(bias), _ptr(out),
         _stream(x.device)))
     return out
+
+
+# -- paged key-value cache -------------------------------------------------------
+KV_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}  # KV_F32 ..
+
+
+class KvCache(ctypes.Structure):
+    """kv_cache of include/w4.h: the pools of one layer's cache."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("weight", _P),
+                ("pages", _I64), ("heads", _I64), ("page_size", _I64), ("head_dim", _I64),
+                ("dtype", ctypes.c_int32)]
+
+
+def _kv_cache(K, V, k_scale, v_scale, weight) -> KvCache:
+    if not isinstance(K, torch.Tensor) or K.dtype not in KV_DTYPES:
+        raise TypeError("K must be a float32, float16, bfloat16 or int8 tensor")
+    _dev(K, K.dtype, "K")
+    _dev(V, K.dtype, "V")
+    shape = K.shape
+    if len(shape) != 4 or V.shape != shape:
+        raise ValueError("K and V must be [pages, heads, page_size, head_dim], of one shape")
+    if K.dtype == torch.int8:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an int8 cache needs k_scale and v_scale")
+        _dev(k_scale, torch.float32, "k_scale")
+        _dev(v_scale, torch.float32, "v_scale")
+        if k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
+            raise ValueError("scales must be [pages, heads, page_size]")
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("only an int8 cache has scales")
+    if weight is not None:
+        _dev(weight, torch.float32, "weight")
+        if weight.shape != shape[:3]:
+            raise ValueError("weight must be [pages, heads, page_size]")
+    return KvCache(_ptr(K), _ptr(V), _ptr(k_scale), _ptr(v_scale), _ptr(weight), *shape,
+                   KV_DTYPES[K.dtype])
+
+
+def _kv_ints(t, name, shape):
+    """An int32 device tensor of the given shape (None: any)."""
+    _dev(t, torch.int32, name)
+    if t.dim() != len(shape) or any(n is not None and m != n for m, n in zip(t.shape, shape)):
+        raise ValueError(f"{name} must be int32 {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _kv_rows(t, name, width):
+    """fp32 [rows, heads, dim] whose rows are dense but may lie apart; (heads, row stride)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a tensor on a HIP device")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != width:
+        raise ValueError(f"{name} must be [rows, heads, {width}]")
+    rows, heads, _ = t.shape
+    stride = t.stride()
+    if stride[2] != 1 or (heads > 1 and stride[1] != width):
+        raise ValueError(f"{name}: a row's heads must be contiguous")
+    return heads, (stride[0] if rows > 1 else heads * width)
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
+              table: torch.Tensor, seq: torch.Tensor, at: torch.Tensor,
+              k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+              weight: torch.Tensor | None = None, d_status: torch.Tensor | None = None) -> None:
+    """Store k, v fp32 [rows, heads, head_dim] (rows may be columns of a fused QKV product) at
+    positions at[r] of sequences seq[r] in the pools K, V [pages, heads, page_size, head_dim]
+    (fp32, fp16, bf16; int8 with scales fp32 [pages, heads, page_size]).  table int32
+    [sequences, columns], seq and at int32 [rows]; weight becomes 0 at the stored positions."""
+    cache = _kv_cache(K, V, k_scale, v_scale, weight)
+    heads, ks = _kv_rows(k, "k", cache.head_dim)
+    heads_v, vs = _kv_rows(v, "v", cache.head_dim)
+    rows = k.shape[0]
+    if heads != cache.heads or heads_v != heads or v.shape[0] != rows:
+        raise ValueError("k and v must be [rows, heads, head_dim] with the cache's heads")
+    _kv_ints(table, "table", (None, None))
+    _kv_ints(seq, "seq", (rows,))
+    _kv_ints(at, "at", (rows,))
+    if d_status is not None:
+        _dev(d_status, torch.int32, "d_status")
+    _check("kv_append", _lib.kv_append(
+        ctypes.byref(cache), _ptr(k), ks, _ptr(v), vs, rows, _ptr(table), *table.shape, _ptr(seq),
+        _ptr(at), _ptr(d_status), _stream(K.device)))
+
+
+def kv_attend(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor,
+              lens: torch.Tensor, starts: torch.Tensor | None = None, scale: float | None = None,
+              max_len: int = 0, k_scale: torch.Tensor | None = None,
+              v_scale: torch.Tensor | None = None, weight: torch.Tensor | None = None,
+              out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+              d_status: torch.Tensor | None = None) -> torch.Tensor:
+    """out fp32 [sequences, q_heads, head_dim]: attention of one new token in each sequence over
+    positions starts[b] (or 0) to lens[b] of the paged cache; pools, table as in kv_append.
+
+    scale: 1 / sqrt(head_dim) by default.  max_len: a bound on lens that the host knows (0: what
+    the table holds); it sets how the length is split.  weight: if given, grows by the attention
+    that each position takes."""
+    cache = _kv_cache(K, V, k_scale, v_scale, weight)
+    q_heads, qs = _kv_rows(q, "q", cache.head_dim)
+    seqs = q.shape[0]
+    _kv_ints(table, "table", (seqs, None))
+    _kv_ints(lens, "lens", (seqs,))
+    if starts is not None:
+        _kv_ints(starts, "starts", (seqs,))
+    if d_status is not None:
+        _dev(d_status, torch.int32, "d_status")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    else:
+        _dev(out, torch.float32, "out")
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    cols = table.shape[1]
+    if workspace is None:
+        most = cols * cache.page_size
+        need = _lib.kv_attend_workspace_bytes(ctypes.byref(cache), seqs, q_heads,
+                                              min(max_len, most) if max_len > 0 else most)
+        ws, wsb = _workspace.get(q.device, need)
+    else:
+        _dev(workspace, torch.uint8, "workspace")
+        ws, wsb = workspace, workspace.numel()
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    _check("kv_attend", _lib.kv_attend(
+        ctypes.byref(cache), _ptr(q), qs, q_heads, _ptr(table), seqs, cols, _ptr(lens),
+        _ptr(starts), max_len, scale, _ptr(out), _ptr(ws), wsb, _ptr(d_status),
+        _stream(K.device)))
+    return out
+
+
+def kv_evict(K: torch.Tensor, V: torch.Tensor, weight: torch.Tensor, table: torch.Tensor,
+             lens: torch.Tensor, keep: int, recent: int, table_out: torch.Tensor,
+             max_len: int = 0, k_scale: torch.Tensor | None = None,
+             v_scale: torch.Tensor | None = None, kept: torch.Tensor | None = None,
+             lens_out: torch.Tensor | None = None, d_status: torch.Tensor | None = None):
+    """Copy the rows that stay, of each sequence longer than `keep` the newest `recent` and those
+    of largest weight, in order to the pages of table_out (none of the pages read).
+
+    -> (kept int32 [sequences, heads, keep]: old positions, then -1; lens_out int32 [sequences])."""
+    if weight is None:
+        raise ValueError("eviction goes by weight")
+    cache = _kv_cache(K, V, k_scale, v_scale, weight)
+    _kv_ints(table, "table", (None, None))
+    seqs, cols = table.shape
+    _kv_ints(lens, "lens", (seqs,))
+    _kv_ints(table_out, "table_out", (seqs, None))
+    if kept is None:
+        kept = torch.empty((seqs, cache.heads, max(keep, 0)), dtype=torch.int32, device=K.device)
+    if lens_out is None:
+        lens_out = torch.empty(seqs, dtype=torch.int32, device=K.device)
+    _kv_ints(kept, "kept", (seqs, cache.heads, keep))
+    _kv_ints(lens_out, "lens_out", (seqs,))
+    if d_status is not None:
+        _dev(d_status, torch.int32, "d_status")
+    _check("kv_evict", _lib.kv_evict(
+        ctypes.byref(cache), _ptr(table), seqs, cols, _ptr(lens), max_len, keep, recent,
+        _ptr(table_out), table_out.shape[1], _ptr(kept), _ptr(lens_out), _ptr(d_status),
+        _stream(K.device)))
+    return kept, lens_out
+
+
+# -- log probabilities -------------------------------------------------------------
+def lp_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0,
+                workspace: torch.Tensor | None = None, d_status: torch.Tensor | None = None):
+    """logits fp32 [M, N] (rows may lie apart) -> (logprob fp32 [M] of tokens int64 [M], or None
+    without tokens; entropy fp32 [M]; top_ids int64 [M, top]; top_logprob fp32 [M, top])."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise TypeError("logits must be a tensor on a HIP device")
+    if logits.dtype != torch.float32:
+        raise TypeError(f"logits must be float32, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [M, N]")
+    M, N = logits.shape
+    if N > 1 and logits.stride(1) != 1:
+        raise ValueError("a row of logits must be contiguous")
+    ld = logits.stride(0) if M > 1 else N
+    dev = logits.device
+    logprob = None
+    if tokens is not None:
+        _dev(tokens, torch.int64, "tokens")
+        if tokens.shape != (M,):
+            raise ValueError("tokens must be [M]")
+        logprob = torch.empty(M, dtype=torch.float32, device=dev)
+    if d_status is not None:
+        _dev(d_status, torch.int32, "d_status")
+    entropy = torch.empty(M, dtype=torch.float32, device=dev)
+    top_ids = torch.empty((M, max(top, 0)), dtype=torch.int64, device=dev)
+    top_logprob = torch.empty((M, max(top, 0)), dtype=torch.float32, device=dev)
+    if workspace is None:
+        ws, wsb = _workspace.get(dev, _lib.lp_logprobs_workspace_bytes(M, N, top))
+    else:
+        _dev(workspace, torch.uint8, "workspace")
+        ws, wsb = workspace, workspace.numel()
+    _check("lp_logprobs", _lib.lp_logprobs(
+        _ptr(logits), M, N, ld, _ptr(tokens), top, _ptr(logprob), _ptr(entropy), _ptr(top_ids),
+        _ptr(top_logprob), _ptr(ws), wsb, _ptr(d_status), _stream(dev)))
+    return logprob, entropy, top_ids, top_logprob

@@ -5,6 +5,7 @@
 #include <atomic>
 #include <string.h>
 
+#include "kv.h"
 #include "launch.h"
 #include "w4.h"
 
@@ -506,6 +507,205 @@ int i8_embed_kmajor(const int64_t *tokens, int64_t T, const int8_t *Qt, int64_t 
     if (st) return st;
     return launched(
         w4::launch_embed_kmajor(tokens, T, Qt, ldt, hs, K, N, out, d_status, as_stream(stream)));
+}
+
+// ---- paged key-value cache ----------------------------------------------------
+// The cache itself: type, sizes, and (for calls that touch the pools) pointers.
+static int check_kv_cache(const kv_cache *c) {
+    if (!c) return W4_ERR_NULL_PTR;
+    if (c->dtype != KV_F32 && c->dtype != KV_F16 && c->dtype != KV_BF16 && c->dtype != KV_I8)
+        return W4_ERR_BAD_SHAPE;
+    if (c->pages < 1 || c->pages > 0x7FFFFFFF || c->heads < 1 || c->heads > 65536)
+        return W4_ERR_BAD_SHAPE;
+    if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)))
+        return W4_ERR_BAD_SHAPE;
+    if (c->head_dim < 8 || c->head_dim > 256 || c->head_dim % 8) return W4_ERR_BAD_SHAPE;
+    if (c->pages > kMaxElems / (c->heads * c->page_size * c->head_dim)) return W4_ERR_BAD_SHAPE;
+    if (!c->k || !c->v || (c->dtype == KV_I8 && (!c->k_scale || !c->v_scale)))
+        return W4_ERR_NULL_PTR;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) ||
+        !aligned(c->v_scale, 4) || !aligned(c->weight, 4))
+        return W4_ERR_MISALIGNED;
+    return W4_OK;
+}
+
+static w4::KvPool as_pool(const kv_cache *c) {
+    w4::KvPool p;
+    p.k = c->k;
+    p.v = c->v;
+    p.k_scale = c->dtype == KV_I8 ? c->k_scale : nullptr;
+    p.v_scale = c->dtype == KV_I8 ? c->v_scale : nullptr;
+    p.weight = c->weight;
+    p.pages = (int)c->pages;
+    p.heads = (int)c->heads;
+    p.shift = __builtin_ctzll((unsigned long long)c->page_size);
+    p.dim = (int)c->head_dim;
+    return p;
+}
+
+// A table of seqs x cols entries, and the bound it and max_len set on lengths.
+static int check_kv_table(const kv_cache *c, int64_t seqs, int64_t cols, int64_t max_len,
+                          int64_t limit) {
+    if (seqs < 0 || seqs > 0x7FFFFFFF || cols < 0 || cols > 0x7FFFFFFF) return W4_ERR_BAD_SHAPE;
+    if (cols > kMaxElems / (seqs > 0 ? seqs : 1)) return W4_ERR_BAD_SHAPE;
+    if (max_len < 0 || max_len > limit) return W4_ERR_BAD_SHAPE;
+    (void)c;
+    return W4_OK;
+}
+
+static int64_t kv_bound(const kv_cache *c, int64_t cols, int64_t max_len, int64_t limit) {
+    int64_t most = cols * c->page_size;
+    if (max_len > 0 && max_len < most) most = max_len;
+    return most < limit ? most : limit;
+}
+
+constexpr int64_t kKvMaxLen = (int64_t)1 << 30;    // attention: positions in int32 with room
+constexpr int64_t kKvMaxEvict = (int64_t)1 << 24;  // eviction
+
+int kv_append(const kv_cache *cache, const float *k, int64_t k_stride, const float *v,
+              int64_t v_stride, int64_t rows, const int32_t *table, int64_t seqs, int64_t cols,
+              const int32_t *seq, const int32_t *at, int *d_status, void *stream) {
+    int st = check_kv_cache(cache);
+    if (st) return st;
+    const int64_t width = cache->heads * cache->head_dim;
+    if (rows < 0 || k_stride < width || v_stride < width) return W4_ERR_BAD_SHAPE;
+    if ((st = check_kv_table(cache, seqs, cols, 0, kKvMaxLen))) return st;
+    if (rows > kMaxElems / k_stride || rows > kMaxElems / v_stride ||
+        rows > 0x7FFFFFFF / cache->heads)
+        return W4_ERR_BAD_SHAPE;
+    if (rows == 0) return W4_OK;
+    if (!k || !v || !need(table, seqs * cols) || !seq || !at) return W4_ERR_NULL_PTR;
+    if (!aligned(k, 4) || !aligned(v, 4) || !aligned(table, 4) || !aligned(seq, 4) ||
+        !aligned(at, 4) || !aligned(d_status, 4))
+        return W4_ERR_MISALIGNED;
+    if ((st = device_check())) return st;
+    return launched(w4::launch_kv_append(as_pool(cache), cache->dtype, k, k_stride, v, v_stride,
+                                         rows, table, seqs, cols, seq, at, d_status,
+                                         as_stream(stream)));
+}
+
+static int check_kv_attend_shape(const kv_cache *cache, int64_t seqs, int64_t q_heads,
+                                 int64_t cols, int64_t max_len) {
+    if (q_heads < 1 || q_heads > 65536 || q_heads % cache->heads) return W4_ERR_BAD_SHAPE;
+    if (seqs < 0 || seqs > 0x7FFFFFFF / q_heads) return W4_ERR_BAD_SHAPE;
+    return check_kv_table(cache, seqs, cols, max_len, kKvMaxLen);
+}
+
+size_t kv_attend_workspace_bytes(const kv_cache *cache, int64_t seqs, int64_t q_heads,
+                                 int64_t max_len) {
+    if (check_kv_cache(cache) || check_kv_attend_shape(cache, seqs, q_heads, 0, max_len)) return 0;
+    return w4::kv_attend_workspace(as_pool(cache), seqs, q_heads, max_len);
+}
+
+int kv_check_attend_args(const kv_cache *cache, const float *q, int64_t q_stride,
+                         int64_t q_heads, const int32_t *table, int64_t seqs, int64_t cols,
+                         const int32_t *lens, const int32_t *starts, int64_t max_len,
+                         const float *out, const void *workspace, size_t workspace_bytes,
+                         const int *d_status) {
+    int st = check_kv_cache(cache);
+    if (st) return st;
+    if ((st = check_kv_attend_shape(cache, seqs, q_heads, cols, max_len))) return st;
+    if (q_stride < q_heads * cache->head_dim) return W4_ERR_BAD_SHAPE;
+    if (seqs > kMaxElems / q_stride) return W4_ERR_BAD_SHAPE;
+    if (seqs == 0) return W4_OK;
+    if (!q || !need(table, cols) || !lens || !out) return W4_ERR_NULL_PTR;
+    if (!aligned(q, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(starts, 4) ||
+        !aligned(out, 4) || !aligned(d_status, 4))
+        return W4_ERR_MISALIGNED;
+    const size_t need_ws = w4::kv_attend_workspace(as_pool(cache), seqs, q_heads,
+                                                   kv_bound(cache, cols, max_len, kKvMaxLen));
+    if (need_ws > 0 && (workspace == nullptr || workspace_bytes < need_ws)) return W4_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return W4_ERR_MISALIGNED;
+    return W4_OK;
+}
+
+int kv_attend(const kv_cache *cache, const float *q, int64_t q_stride, int64_t q_heads,
+              const int32_t *table, int64_t seqs, int64_t cols, const int32_t *lens,
+              const int32_t *starts, int64_t max_len, float scale, float *out, void *workspace,
+              size_t workspace_bytes, int *d_status, void *stream) {
+    int st = kv_check_attend_args(cache, q, q_stride, q_heads, table, seqs, cols, lens, starts,
+                                  max_len, out, workspace, workspace_bytes, d_status);
+    if (st) return st;
+    if (seqs == 0) return W4_OK;
+    if ((st = device_check())) return st;
+    return launched(w4::launch_kv_attend(as_pool(cache), cache->dtype, q, q_stride, q_heads,
+                                         table, seqs, cols, lens, starts,
+                                         kv_bound(cache, cols, max_len, kKvMaxLen), scale, out,
+                                         workspace, d_status, as_stream(stream)));
+}
+
+int kv_evict(const kv_cache *cache, const int32_t *table, int64_t seqs, int64_t cols,
+             const int32_t *lens, int64_t max_len, int64_t keep, int64_t recent,
+             const int32_t *table_out, int64_t cols_out, int32_t *kept, int32_t *lens_out,
+             int *d_status, void *stream) {
+    int st = check_kv_cache(cache);
+    if (st) return st;
+    if (!cache->weight) return W4_ERR_NULL_PTR;
+    if ((st = check_kv_table(cache, seqs, cols, max_len, kKvMaxEvict))) return st;
+    if ((st = check_kv_table(cache, seqs, cols_out, 0, kKvMaxEvict))) return st;
+    if (keep < 1 || keep > kKvMaxEvict || recent < 0 || seqs > 65535 / cache->heads)
+        return W4_ERR_BAD_SHAPE;
+    const int64_t most = kv_bound(cache, cols, max_len, kKvMaxEvict);
+    if (cols_out * cache->page_size < (keep < most ? keep : most)) return W4_ERR_BAD_SHAPE;
+    if (seqs == 0) return W4_OK;
+    if (!need(table, cols) || !lens || !need(table_out, cols_out) || !kept || !lens_out)
+        return W4_ERR_NULL_PTR;
+    if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(table_out, 4) || !aligned(kept, 4) ||
+        !aligned(lens_out, 4) || !aligned(d_status, 4))
+        return W4_ERR_MISALIGNED;
+    if ((st = device_check())) return st;
+    static const int kElem[4] = {4, 2, 2, 1};
+    return launched(w4::launch_kv_evict(
+        as_pool(cache), (int)cache->head_dim * kElem[cache->dtype], table, seqs, cols, lens, most,
+        keep, recent < keep ? recent : keep, table_out, cols_out, kept, lens_out, d_status,
+        as_stream(stream)));
+}
+
+// ---- log probabilities ----------------------------------------------------------
+static int check_logprobs_shape(int64_t M, int64_t N, int64_t top) {
+    if (M < 0 || M > 0x7FFFFFFF || N < 0 || N > 0x7FFFFFFF) return W4_ERR_BAD_SHAPE;
+    if (M > 0 && N < 1) return W4_ERR_BAD_SHAPE;
+    if (top < 0 || top > LP_MAX_TOP || (M > 0 && top > N)) return W4_ERR_BAD_SHAPE;
+    return W4_OK;
+}
+
+size_t lp_logprobs_workspace_bytes(int64_t M, int64_t N, int64_t top) {
+    if (check_logprobs_shape(M, N, top) || M == 0) return 0;
+    return w4::logprobs_workspace(M, N, top);
+}
+
+int lp_check_logprobs_args(const float *logits, int64_t M, int64_t N, int64_t ld,
+                           const int64_t *tokens, int64_t top, const float *logprob,
+                           const float *entropy, const int64_t *top_ids,
+                           const float *top_logprob, const void *workspace,
+                           size_t workspace_bytes, const int *d_status) {
+    int st = check_logprobs_shape(M, N, top);
+    if (st) return st;
+    if (ld < N || M > kMaxElems / (ld > 0 ? ld : 1)) return W4_ERR_BAD_SHAPE;
+    if (M == 0) return W4_OK;
+    if (!logits || (logprob && !tokens) || (top > 0 && (!top_ids || !top_logprob)))
+        return W4_ERR_NULL_PTR;
+    if (!aligned(logits, 4) || !aligned(tokens, 8) || !aligned(logprob, 4) ||
+        !aligned(entropy, 4) || !aligned(top_ids, 8) || !aligned(top_logprob, 4) ||
+        !aligned(d_status, 4))
+        return W4_ERR_MISALIGNED;
+    const size_t need_ws = w4::logprobs_workspace(M, N, top);
+    if (need_ws > 0 && (workspace == nullptr || workspace_bytes < need_ws)) return W4_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return W4_ERR_MISALIGNED;
+    return W4_OK;
+}
+
+int lp_logprobs(const float *logits, int64_t M, int64_t N, int64_t ld, const int64_t *tokens,
+                int64_t top, float *logprob, float *entropy, int64_t *top_ids,
+                float *top_logprob, void *workspace, size_t workspace_bytes, int *d_status,
+                void *stream) {
+    int st = lp_check_logprobs_args(logits, M, N, ld, tokens, top, logprob, entropy, top_ids,
+                                    top_logprob, workspace, workspace_bytes, d_status);
+    if (st) return st;
+    if (M == 0) return W4_OK;
+    if ((st = device_check())) return st;
+    return launched(w4::launch_logprobs(logits, M, N, ld, tokens, top, logprob, entropy, top_ids,
+                                        top_logprob, workspace, d_status, as_stream(stream)));
 }
 
 size_t w4_read_bytes_words(int64_t bytes, int loads_per_lane) {

@@ -75,6 +75,31 @@ hipError_t launch_embed_kmajor(const int64_t *tokens, int64_t T, const int8_t *Q
                                const float *hs, int64_t K, int64_t N, float *out, int *d_status,
                                hipStream_t stream);
 
+// Paged key-value cache (kv.h): append, attention of one new token in each
+// sequence, eviction.  max_len is already the effective bound on lens.
+struct KvPool;
+hipError_t launch_kv_append(const KvPool &c, int dtype, const float *k, int64_t k_stride,
+                            const float *v, int64_t v_stride, int64_t rows, const int32_t *table,
+                            int64_t seqs, int64_t cols, const int32_t *seq, const int32_t *at,
+                            int *d_status, hipStream_t stream);
+size_t kv_attend_workspace(const KvPool &c, int64_t seqs, int64_t q_heads, int64_t max_len);
+hipError_t launch_kv_attend(const KvPool &c, int dtype, const float *q, int64_t q_stride,
+                            int64_t q_heads, const int32_t *table, int64_t seqs, int64_t cols,
+                            const int32_t *lens, const int32_t *starts, int64_t max_len,
+                            float scale, float *out, void *workspace, int *d_status,
+                            hipStream_t stream);
+hipError_t launch_kv_evict(const KvPool &c, int row_bytes, const int32_t *table, int64_t seqs,
+                           int64_t cols, const int32_t *lens, int64_t max_len, int64_t keep,
+                           int64_t recent, const int32_t *table_out, int64_t cols_out,
+                           int32_t *kept, int32_t *lens_out, int *d_status, hipStream_t stream);
+
+// Log probabilities of given tokens, entropy and the largest entries.
+size_t logprobs_workspace(int64_t M, int64_t N, int64_t top);
+hipError_t launch_logprobs(const float *logits, int64_t M, int64_t N, int64_t ld,
+                           const int64_t *tokens, int64_t top, float *logprob, float *entropy,
+                           int64_t *top_ids, float *top_logprob, void *workspace, int *d_status,
+                           hipStream_t stream);
+
 // Streaming-read reference: `loads` 16-byte loads per lane, 256 lanes per
 // workgroup, one XOR word per wave into out[read_bytes_words(...)].
 int64_t read_bytes_groups(int64_t bytes, int loads);
