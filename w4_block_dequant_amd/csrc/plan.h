@@ -99,4 +99,17 @@ struct X3Plan {
 
 X3Plan plan_x3(int64_t M, int64_t K, int64_t N);
 
+// ---- attention over the paged cache ------------------------------------------
+// The bound on the lengths is cut into `splits` stretches of split_len
+// positions (a multiple of 128); offsets of the workspace's arrays: (m, l) of
+// every (sequence, query head, stretch), their sums p v (splits > 1), and the
+// scores [seqs, q_heads, score_stride] (weigh).
+struct KvAttendPlan {
+    int64_t splits = 1, split_len = 128, score_stride = 0;
+    size_t stats = 0, part = 0, scores = 0, workspace = 0;
+};
+
+KvAttendPlan plan_kv_attend(int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim,
+                            int64_t max_len, bool weigh);
+
 }  // namespace w4
