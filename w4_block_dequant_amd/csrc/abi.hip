@@ -606,6 +606,10 @@ int kv_check_attend_args(const kv_cache *cache, const float *q, int64_t q_stride
     if (st) return st;
     if ((st = check_kv_attend_shape(cache, seqs, q_heads, cols, max_len))) return st;
     if (q_stride < q_heads * cache->head_dim) return W4_ERR_BAD_SHAPE;
+    // the work list is counted in int32
+    if (w4::kv_attend_units(seqs, q_heads, cache->heads,
+                            kv_bound(cache, cols, max_len, kKvMaxLen)) > 0x7FFFFFFF)
+        return W4_ERR_BAD_SHAPE;
     if (seqs > kMaxElems / q_stride) return W4_ERR_BAD_SHAPE;
     if (seqs == 0) return W4_OK;
     if (!q || !need(table, cols) || !lens || !out) return W4_ERR_NULL_PTR;

@@ -459,27 +459,33 @@ X3Plan plan_x3(int64_t M, int64_t K, int64_t N) {
     return p;
 }
 
+int64_t kv_attend_units(int64_t seqs, int64_t q_heads, int64_t heads, int64_t max_len) {
+    return seqs * heads * cdiv(q_heads / heads, 16) * (cdiv(max_len, 128) + kKvOpenUnits);
+}
+
 KvAttendPlan plan_kv_attend(int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim,
                             int64_t max_len, bool weigh) {
     KvAttendPlan p;
     if (seqs <= 0) return p;
-    // enough stretches that every compute unit has several workgroups, none
-    // shorter than 256 positions (two tiles for each wave)
-    constexpr int64_t kTargetWgs = 2048, kShortest = 256;
-    const int64_t lanes = seqs * heads * cdiv(q_heads / heads, 16);
-    int64_t splits = kTargetWgs / lanes;
-    if (splits > cdiv(max_len, kShortest)) splits = cdiv(max_len, kShortest);
-    if (splits < 1) splits = 1;
-    p.split_len = (int64_t)align_up((size_t)cdiv(max_len > 0 ? max_len : 1, splits), 128);
-    p.splits = cdiv(max_len > 0 ? max_len : 1, p.split_len);
+    // as many workgroups as fit the chip at once, if there are steps for them
+    const int64_t fit = 256 * (dim <= 64 ? 3 : dim <= 128 ? 2 : 1);
+    p.groups = seqs * heads * cdiv(q_heads / heads, 16) * cdiv(max_len > 0 ? max_len : 1, 128);
+    if (p.groups > fit) p.groups = fit;
+    p.split = max_len > 128;
     p.score_stride = (int64_t)align_up((size_t)max_len, 32);
     const size_t rows = (size_t)(seqs * q_heads);
+    const size_t blocks = (size_t)(seqs * heads * cdiv(q_heads / heads, 16));
     size_t at = 0;
-    if (p.splits > 1 || weigh) at += align_up(rows * (size_t)splits * 8, 256);
-    p.part = at;
-    if (p.splits > 1) at += align_up(rows * (size_t)splits * (size_t)dim * 4, 256);
-    p.scores = at;
-    if (weigh) at += align_up(rows * (size_t)p.score_stride * 4, 256);
+    auto take = [&](bool wanted, size_t bytes) {
+        const size_t here = at;
+        if (wanted) at += align_up(bytes, 256);
+        return here;
+    };
+    p.stat = take(p.split, (size_t)p.groups * 2 * 16 * 8);
+    p.sum = take(p.split, (size_t)p.groups * 2 * 16 * 4 * (size_t)dim);
+    p.owner = take(p.split || weigh, blocks * 8);
+    p.whole = take(weigh, rows * 8);
+    p.scores = take(weigh, rows * 4 * (size_t)p.score_stride);
     p.workspace = at;
     return p;
 }

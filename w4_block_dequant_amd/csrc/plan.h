@@ -100,14 +100,20 @@ struct X3Plan {
 X3Plan plan_x3(int64_t M, int64_t K, int64_t N);
 
 // ---- attention over the paged cache ------------------------------------------
-// The bound on the lengths is cut into `splits` stretches of split_len
-// positions (a multiple of 128); offsets of the workspace's arrays: (m, l) of
-// every (sequence, query head, stretch), their sums p v (splits > 1), and the
-// scores [seqs, q_heads, score_stride] (weigh).
+// `groups` workgroups share the list of units (128 positions of one row block
+// of at most 16 query heads, and kKvOpenUnits for each block's own cost); `split`:
+// a block may cross workgroups, so a second kernel joins; offsets of the
+// workspace's arrays (KvParts in kvattend.hip).
+constexpr int kKvOpenUnits = 2, kKvPartSteps = 4;
+
 struct KvAttendPlan {
-    int64_t splits = 1, split_len = 128, score_stride = 0;
-    size_t stats = 0, part = 0, scores = 0, workspace = 0;
+    int64_t groups = 0, score_stride = 0;
+    bool split = false;
+    size_t stat = 0, sum = 0, owner = 0, whole = 0, scores = 0, workspace = 0;
 };
+
+// Units of the list if every length is max_len (the kernels count in int32).
+int64_t kv_attend_units(int64_t seqs, int64_t q_heads, int64_t heads, int64_t max_len);
 
 KvAttendPlan plan_kv_attend(int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim,
                             int64_t max_len, bool weigh);
