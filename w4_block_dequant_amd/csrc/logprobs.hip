@@ -1,10 +1,33 @@
 // Log probabilities of given tokens, entropy and the largest entries, read off
-// the head's logits (see include/w4.h).  With m = max x, S = sum e^(x-m):
-//   log p = (x - m) - log S,   entropy = log S - (sum e^(x-m) (x-m)) / S.
+// the head's logits (see include/w4.h).  With m = max x, S = sum e^(x-m),
+// W = sum e^(x-m) (x-m):
+//   log p = (x - m) - log S,   entropy = log S - W / S.
 //
-// One workgroup takes one row: its maximum, then the two sums, then one pass
-// for each of the largest entries (the largest key below the last one; a key
-// holds the value and the inverted index, so ties go to the lower index).
+// Bound: the logits' bytes, read once.  One workgroup of 8 waves takes a row, or
+// one of the `chunks` pieces of a row where there are few rows; a second kernel
+// then joins the pieces in order.  A lane holds 16 logits of its wave's 1024 at
+// a time, with the next 16 already on their way, and keeps (m, S, W) of what it
+// has seen, rescaled once for each 16.
+//
+// The largest entries.  A key is the value in an order that unsigned integers
+// have, then the inverted index: keys are distinct and the larger key is the
+// larger value or, of equal ones, the lower index.  Each wave holds its 64
+// largest keys in descending order, one in a lane, and a queue of new ones.  A
+// logit is looked at again only if its lane's largest of 16 reaches the
+// threshold, a key that at least `top` keys of the row reach: at first the
+// top-th largest of the wave's lane maxima, later the top-th key of the list
+// or, if that is larger, any other wave's.  Keys past the threshold enter the
+// queue; at 64 they are sorted and merged into the list (of 50,000 logits drawn
+// alike some hundred ever enter a queue).  Which keys get so far depends on
+// the waves' timing, the `top` largest do not.
+//
+// Sorting exchanges lanes by DPP and permlane swaps: compare-and-exchange with
+// lane ^ (2^i - 1), then lane ^ 2^j downwards, so that every step keeps the
+// larger key in the lower lane.
+//
+// NaN or +infinity makes S NaN (x - m = infinity - infinity), and nothing else
+// does: a -infinity gives e = 0, and in W a difference below -1e30 counts as
+// -1e30, whose e is 0.
 #include <math.h>
 
 #include "kv.h"
@@ -13,94 +36,379 @@
 namespace w4 {
 namespace {
 
-constexpr int kThreads = 256;
+typedef float f32x4u_t __attribute__((ext_vector_type(4), aligned(4)));
 
-template <class T, class F>
-__device__ __forceinline__ T block_reduce(T v, T *s, F f) {
-    __syncthreads();
-    s[threadIdx.x] = v;
-    __syncthreads();
-    for (int o = kThreads / 2; o > 0; o >>= 1) {
-        if (threadIdx.x < (unsigned)o) s[threadIdx.x] = f(s[threadIdx.x], s[threadIdx.x + o]);
-        __syncthreads();
+constexpr int kLpWaves = 8;
+constexpr int kLpLoads = 4;  // 16-byte loads of a lane in flight
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ---- lane exchanges --------------------------------------------------------------
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+// v of lane ^ X, X a power of two or one less than one.
+template <int X>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v) {
+    if constexpr (X == 1) {
+        return dpp<0xB1>(v);  // quad_perm 1 0 3 2
+    } else if constexpr (X == 2) {
+        return dpp<0x4E>(v);  // quad_perm 2 3 0 1
+    } else if constexpr (X == 3) {
+        return dpp<0x1B>(v);  // quad_perm 3 2 1 0
+    } else if constexpr (X == 4) {
+        return dpp<0x141>(dpp<0x1B>(v));
+    } else if constexpr (X == 7) {
+        return dpp<0x141>(v);  // mirror in 8
+    } else if constexpr (X == 8) {
+        return dpp<0x128>(v);  // rotation by 8 in 16
+    } else if constexpr (X == 15) {
+        return dpp<0x140>(v);  // mirror in 16
+    } else if constexpr (X == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return threadIdx.x & 16 ? r[0] : r[1];
+    } else if constexpr (X == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return threadIdx.x & 32 ? r[0] : r[1];
+    } else if constexpr (X == 31) {
+        return lane_xor<16>(dpp<0x140>(v));
+    } else {
+        static_assert(X == 63, "");
+        return lane_xor<32>(lane_xor<16>(dpp<0x140>(v)));
     }
-    return s[0];
+}
+template <int X>
+__device__ __forceinline__ uint64_t lane_xor(uint64_t v) {
+    return (uint64_t)lane_xor<X>((uint32_t)(v >> 32)) << 32 | lane_xor<X>((uint32_t)v);
+}
+template <int X>
+__device__ __forceinline__ float lane_xor(float v) {
+    return __builtin_bit_cast(float, lane_xor<X>(__builtin_bit_cast(uint32_t, v)));
 }
 
-__global__ __launch_bounds__(kThreads) void k_logprobs(const float *logits, int64_t N, int64_t ld,
-                                                       const int64_t *tokens, int top,
-                                                       float *logprob, float *entropy,
-                                                       int64_t *top_ids, float *top_logprob,
-                                                       int *d_status) {
-    __shared__ float sf[kThreads];
-    __shared__ uint64_t su[kThreads];
-    const int64_t row = blockIdx.x;
-    const float *x = logits + row * ld;
-    float m = -INFINITY;
-    int bad = 0;
-    for (int64_t n = threadIdx.x; n < N; n += kThreads) {
-        bad |= !(x[n] < INFINITY);
-        m = fmaxf(m, x[n]);
-    }
-    m = block_reduce(m, sf, [](float a, float b) { return fmaxf(a, b); });
-    bad = block_reduce((float)bad, sf, [](float a, float b) { return a + b; }) != 0.0f;
-    const bool none = m == -INFINITY && !bad;
-    float S = 0.0f, W = 0.0f;
-    for (int64_t n = threadIdx.x; n < N; n += kThreads) {
-        const float d = x[n] - m;  // -infinity where the difference passes fp32
-        const float e = expf(d);
-        if (e > 0.0f) {
-            S += e;
-            W += e * d;
-        }
-    }
-    auto add = [](float a, float b) { return a + b; };
-    S = block_reduce(S, sf, add);
-    W = block_reduce(W, sf, add);
-    const float logS = logf(S);
+// The larger of the pair stays in the lane whose bit BIT is clear.
+template <int X, int BIT, class K>
+__device__ __forceinline__ void exchange(K &v) {
+    const K o = lane_xor<X>(v);
+    const bool up = threadIdx.x & BIT;
+    v = (o > v) != up ? o : v;
+}
+// A bitonic sequence into descending order over the wave.
+template <class K>
+__device__ __forceinline__ void clean64(K &v) {
+    exchange<32, 32>(v);
+    exchange<16, 16>(v);
+    exchange<8, 8>(v);
+    exchange<4, 4>(v);
+    exchange<2, 2>(v);
+    exchange<1, 1>(v);
+}
+template <class K>
+__device__ __forceinline__ void sort64(K &v) {
+    exchange<1, 1>(v);
+    exchange<3, 2>(v);
+    exchange<1, 1>(v);
+    exchange<7, 4>(v);
+    exchange<2, 2>(v);
+    exchange<1, 1>(v);
+    exchange<15, 8>(v);
+    exchange<4, 4>(v);
+    exchange<2, 2>(v);
+    exchange<1, 1>(v);
+    exchange<31, 16>(v);
+    exchange<8, 8>(v);
+    exchange<4, 4>(v);
+    exchange<2, 2>(v);
+    exchange<1, 1>(v);
+    exchange<63, 32>(v);
+    exchange<16, 16>(v);
+    exchange<8, 8>(v);
+    exchange<4, 4>(v);
+    exchange<2, 2>(v);
+    exchange<1, 1>(v);
+}
+// The 64 largest of a descending list and a descending list given in reverse.
+__device__ __forceinline__ void merge64(uint64_t &list, uint64_t reversed) {
+    list = list > reversed ? list : reversed;
+    clean64(list);
+}
+
+__device__ __forceinline__ uint64_t lane_key(uint64_t v, int lane) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+}
+
+// ---- maximum and sums ------------------------------------------------------------
+struct LpSums {
+    float m, S, W;
+};
+__device__ __forceinline__ float pow_e(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
+// Of two disjoint parts; a part that holds nothing but -infinity has S = 0.
+__device__ __forceinline__ LpSums lp_join(const LpSums &a, const LpSums &b) {
+    LpSums r;
+    r.m = fmaxf(a.m, b.m);
+    const float da = a.m == -INFINITY ? -1e30f : fmaxf(a.m - r.m, -1e30f);
+    const float db = b.m == -INFINITY ? -1e30f : fmaxf(b.m - r.m, -1e30f);
+    const float ea = pow_e(da), eb = pow_e(db);
+    r.S = ea * a.S + eb * b.S;
+    r.W = ea * fmaf(da, a.S, a.W) + eb * fmaf(db, b.S, b.W);
+    // an infinite maximum: infinity - infinity, which S reports
+    if (r.m == INFINITY) r.S = NAN;
+    return r;
+}
+template <int X>
+__device__ __forceinline__ LpSums lp_join_lanes(const LpSums &a) {
+    const LpSums b = {lane_xor<X>(a.m), lane_xor<X>(a.S), lane_xor<X>(a.W)};
+    return threadIdx.x & X ? lp_join(b, a) : lp_join(a, b);  // the same sum in both lanes
+}
+__device__ __forceinline__ LpSums lp_wave(LpSums a) {
+    a = lp_join_lanes<1>(a);
+    a = lp_join_lanes<2>(a);
+    a = lp_join_lanes<4>(a);
+    a = lp_join_lanes<8>(a);
+    a = lp_join_lanes<16>(a);
+    return lp_join_lanes<32>(a);
+}
+
+struct LpOut {
+    const int64_t *tokens;
+    float *logprob, *entropy, *top_logprob;
+    int64_t *top_ids;
+    int *d_status;
+};
+
+// What a row's maximum, sums and list come to; wave 0 of a workgroup.
+__device__ __forceinline__ void lp_finish(const LpOut &o, int64_t row, const float *x, int64_t N,
+                                          int top, const LpSums &r, uint64_t list) {
+    const int lane = threadIdx.x;
+    const bool bad = __builtin_isnan(r.S), none = r.m == -INFINITY && !bad;
+    const float logS = logf(r.S);
     auto log_p = [&](float v) {
-        return bad ? NAN : none || v == -INFINITY ? -INFINITY : (v - m) - logS;
+        return bad ? NAN : none || v == -INFINITY ? -INFINITY : (v - r.m) - logS;
     };
-    if (threadIdx.x == 0) {
-        if (bad) set_status(d_status, W4_ERR_NONFINITE);
-        if (logprob) {
-            const int64_t token = tokens[row];
+    if (lane == 0) {
+        if (bad) set_status(o.d_status, W4_ERR_NONFINITE);
+        if (o.logprob) {
+            const int64_t token = o.tokens[row];
             const bool in = token >= 0 && token < N;
-            if (!in) set_status(d_status, W4_ERR_BAD_SHAPE);
-            logprob[row] = in ? log_p(x[token]) : NAN;
+            if (!in) set_status(o.d_status, W4_ERR_BAD_SHAPE);
+            o.logprob[row] = in ? log_p(x[token]) : NAN;
         }
-        if (entropy) entropy[row] = bad ? NAN : none ? 0.0f : logS - W / S;
+        if (o.entropy) o.entropy[row] = bad ? NAN : none ? 0.0f : logS - r.W / r.S;
     }
-    uint64_t last = ~0ull;
-    for (int j = 0; j < top; ++j) {
-        uint64_t best = 0;
-        for (int64_t n = threadIdx.x; n < N; n += kThreads) {
-            const uint64_t key = (uint64_t)order_key(x[n]) << 32 | (uint32_t)~(uint32_t)n;
-            if (key < last && key > best) best = key;
+    if (lane < top) {
+        o.top_ids[row * top + lane] = bad ? -1 : (int64_t)(uint32_t)~(uint32_t)list;
+        o.top_logprob[row * top + lane] = log_p(order_value((uint32_t)(list >> 32)));
+    }
+}
+
+// Grid: rows x chunks.  chunks == 1: straight to the outputs; else (m, S, W)
+// and the `top` largest keys of each chunk to the workspace.
+__global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restrict__ logits,
+                                                            int64_t N, int64_t ld, int top,
+                                                            int chunks, int chunk, LpOut o,
+                                                            float4 *sums, uint64_t *keys) {
+    __shared__ uint64_t s_key[kLpWaves][128];  // queues, later lists
+    __shared__ uint64_t s_limit;
+    __shared__ LpSums s_sum[kLpWaves];
+    const int64_t row = blockIdx.x / chunks;
+    const int piece = (int)(blockIdx.x % chunks);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const float *x = logits + row * ld;
+    // 32 bits unsigned: N is below 2^31 and a wave looks at most 2^14 ahead of it
+    const uint32_t begin = (uint32_t)piece * (uint32_t)chunk;
+    const uint32_t end = min(begin + (uint32_t)chunk, (uint32_t)N);
+    if (threadIdx.x == 0) s_limit = 0;
+    __syncthreads();
+
+    LpSums r = {-INFINITY, 0.0f, 0.0f};
+    uint64_t list = 0, limit = 0;  // descending keys; the threshold (0: none yet)
+    float reach = -INFINITY;       // its value
+    int queued = 0;
+    bool fresh = true;
+    auto raise = [&](uint64_t to) {
+        if (to > limit) {
+            limit = to;
+            reach = order_value((uint32_t)(limit >> 32));
         }
-        best = block_reduce(best, su, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
-        last = best;
-        if (threadIdx.x == 0) {
-            top_ids[row * top + j] = bad ? -1 : (int64_t)(uint32_t)~(uint32_t)best;
-            top_logprob[row * top + j] = log_p(order_value((uint32_t)(best >> 32)));
+    };
+    auto flush = [&]() {
+        // the wave's own LDS writes, in order: only the compiler has to wait
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        uint64_t v = lane < queued ? s_key[wave][lane] : 0;
+        sort64(v);
+        merge64(list, lane_xor<63>(v));
+        queued = max(queued - 64, 0);
+        if (lane < queued) s_key[wave][lane] = s_key[wave][64 + lane];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        const uint64_t own = lane_key(list, top - 1);
+        if (own > limit) {
+            if (lane == 0) atomicMax((unsigned long long *)&s_limit, (unsigned long long)own);
+            raise(own);
+        }
+    };
+
+    constexpr int kSpan = 256 * kLpLoads;  // logits of a wave at a time
+    f32x4_t next[kLpLoads];
+    auto load = [&](uint32_t at) {
+        // a lane's load j is logits at + 256 j + 4 lane ..; past the end: -infinity
+#pragma unroll
+        for (int j = 0; j < kLpLoads; ++j) {
+            const uint32_t n = at + 256 * j + 4 * lane;
+            if (at + kSpan <= end) {
+                next[j] = __builtin_nontemporal_load((const f32x4u_t *)(x + n));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    next[j][i] = n + i < end ? x[n + i] : -INFINITY;
+            }
+        }
+    };
+    uint32_t at = begin + wave * kSpan;
+    if (at < end) load(at);
+    for (; at < end; at += kLpWaves * kSpan) {
+        f32x4_t v[kLpLoads];
+#pragma unroll
+        for (int j = 0; j < kLpLoads; ++j) v[j] = next[j];
+        if (at + kLpWaves * kSpan < end) load(at + kLpWaves * kSpan);
+        float best = v[0][0];
+#pragma unroll
+        for (int j = 0; j < 4 * kLpLoads; ++j) best = fmaxf(best, v[j / 4][j % 4]);
+        if (best > r.m) {
+            const float d = r.m == -INFINITY ? 0.0f : r.m - best;
+            const float f = r.m == -INFINITY ? 0.0f : pow_e(d);
+            r.W = f * fmaf(fmaxf(d, -1e30f), r.S, r.W);
+            r.S *= f;
+            r.m = best;
+        }
+        const float ref = r.m == -INFINITY ? 0.0f : r.m;
+#pragma unroll
+        for (int j = 0; j < 4 * kLpLoads; ++j) {
+            const float d = v[j / 4][j % 4] - ref;
+            const float e = pow_e(d);
+            r.S += e;
+            r.W = fmaf(e, fmaxf(d, -1e30f), r.W);
+        }
+        if (top > 0) {
+            if (fresh) {
+                uint32_t first = order_key(best);
+                sort64(first);
+                const uint64_t to =
+                    (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)first, top - 1) << 32;
+                if (lane == 0) atomicMax((unsigned long long *)&s_limit, (unsigned long long)to);
+                raise(to);
+                fresh = false;
+            }
+            raise(*(volatile uint64_t *)&s_limit);
+            if (__any(best >= reach)) {
+                uint32_t bits = 0;  // of a lane's 16 that may pass
+#pragma unroll
+                for (int j = 0; j < 4 * kLpLoads; ++j)
+                    bits |= v[j / 4][j % 4] >= reach ? 1u << j : 0u;
+                while (__any(bits != 0)) {
+                    const int j = bits ? __builtin_ctz(bits) : 0;
+                    float w = v[0][0];  // v[j / 4][j % 4] without indexed registers
+#pragma unroll
+                    for (int i = 1; i < 4 * kLpLoads; ++i)
+                        if (i == j) w = v[i / 4][i % 4];
+                    const uint32_t n = at + 256 * (j / 4) + 4 * lane + j % 4;
+                    const uint64_t key = (uint64_t)order_key(w) << 32 | (uint32_t)~n;
+                    const bool in = bits != 0 && n < end && key > limit;
+                    bits &= bits - 1;
+                    const uint64_t mask = __ballot(in);
+                    if (!mask) continue;
+                    if (in)
+                        s_key[wave][queued + __builtin_amdgcn_mbcnt_hi(
+                                                 (uint32_t)(mask >> 32),
+                                                 __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] =
+                            key;
+                    queued += __popcll(mask);
+                    if (queued >= 64) flush();
+                }
+            }
         }
     }
+    if (top > 0 && queued > 0) flush();
+    r = lp_wave(r);
+    if (lane == 0) s_sum[wave] = r;
+    if (top > 0) {
+        // the waves' lists, two by two
+#pragma unroll
+        for (int half = kLpWaves / 2; half > 0; half >>= 1) {
+            if (wave >= half && wave < 2 * half) s_key[wave][lane] = list;
+            __syncthreads();
+            if (wave < half) merge64(list, s_key[wave + half][63 - lane]);
+        }
+    } else {
+        __syncthreads();
+    }
+    if (wave != 0) return;
+    r = s_sum[0];
+#pragma unroll
+    for (int w = 1; w < kLpWaves; ++w) r = lp_join(r, s_sum[w]);
+    if (chunks == 1) {
+        lp_finish(o, row, x, N, top, r, list);
+    } else {
+        if (lane == 0) sums[blockIdx.x] = make_float4(r.m, r.S, r.W, 0.0f);
+        if (lane < top) keys[(int64_t)blockIdx.x * top + lane] = list;
+    }
+}
+
+// One workgroup joins the chunks of a row: its four waves take every fourth
+// chunk's list, which is in descending order already.
+__global__ __launch_bounds__(256) void k_logprobs_join(const float *__restrict__ logits, int64_t N,
+                                                       int64_t ld, int top, int chunks, LpOut o,
+                                                       const float4 *__restrict__ sums,
+                                                       const uint64_t *__restrict__ keys) {
+    __shared__ uint64_t s_key[4][64];
+    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint64_t list = 0;
+    if (top > 0) {
+        for (int i = wave; i < chunks; i += 4) {
+            const uint64_t k =
+                63 - lane < top ? keys[(row * chunks + i) * top + 63 - lane] : 0;
+            merge64(list, k);
+        }
+#pragma unroll
+        for (int half = 2; half > 0; half >>= 1) {
+            if (wave >= half && wave < 2 * half) s_key[wave][lane] = list;
+            __syncthreads();
+            if (wave < half) merge64(list, s_key[wave + half][63 - lane]);
+        }
+    }
+    if (wave != 0) return;
+    LpSums r = {-INFINITY, 0.0f, 0.0f};
+    for (int i = lane; i < chunks; i += 64) {
+        const float4 v = sums[row * chunks + i];
+        r = lp_join(r, LpSums{v.x, v.y, v.z});
+    }
+    r = lp_wave(r);
+    lp_finish(o, row, logits + row * ld, N, top, r, list);
 }
 
 }  // namespace
 
 size_t logprobs_workspace(int64_t M, int64_t N, int64_t top) {
-    (void)M, (void)N, (void)top;
-    return 0;
+    const LogprobsPlan p = plan_logprobs(M, N, top);
+    return p.workspace;
 }
 
 hipError_t launch_logprobs(const float *logits, int64_t M, int64_t N, int64_t ld,
                            const int64_t *tokens, int64_t top, float *logprob, float *entropy,
                            int64_t *top_ids, float *top_logprob, void *workspace, int *d_status,
                            hipStream_t stream) {
-    (void)workspace;
-    hipLaunchKernelGGL(k_logprobs, dim3((unsigned)M), dim3(kThreads), 0, stream, logits, N, ld,
-                       tokens, (int)top, logprob, entropy, top_ids, top_logprob, d_status);
+    const LogprobsPlan p = plan_logprobs(M, N, top);
+    const LpOut o = {tokens, logprob, entropy, top_logprob, top_ids, d_status};
+    float4 *sums = p.chunks > 1 ? (float4 *)workspace : nullptr;
+    uint64_t *keys = p.chunks > 1 ? (uint64_t *)((char *)workspace + p.keys) : nullptr;
+    hipLaunchKernelGGL(k_logprobs, dim3((unsigned)(M * p.chunks)), dim3(64 * kLpWaves), 0, stream,
+                       logits, N, ld, (int)top, (int)p.chunks, (int)p.chunk, o, sums, keys);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.chunks == 1) return e;
+    hipLaunchKernelGGL(k_logprobs_join, dim3((unsigned)M), dim3(256), 0, stream, logits, N, ld,
+                       (int)top, (int)p.chunks, o, sums, keys);
     return hipGetLastError();
 }
 

@@ -490,4 +490,21 @@ KvAttendPlan plan_kv_attend(int64_t seqs, int64_t q_heads, int64_t heads, int64_
     return p;
 }
 
+LogprobsPlan plan_logprobs(int64_t M, int64_t N, int64_t top) {
+    LogprobsPlan p;
+    p.chunk = N;
+    if (M <= 0) return p;
+    // two workgroups for each compute unit, none with less than 2048 logits
+    constexpr int64_t kWgs = 512, kLeast = 2048;
+    int64_t chunks = kWgs / M;
+    if (chunks > N / kLeast) chunks = N / kLeast;
+    if (chunks <= 1) return p;
+    p.chunk = (int64_t)align_up((size_t)cdiv(N, chunks), 256);
+    p.chunks = cdiv(N, p.chunk);
+    if (p.chunks == 1) return p;
+    p.keys = align_up((size_t)(M * p.chunks) * 16, 256);
+    p.workspace = p.keys + align_up((size_t)(M * p.chunks * top) * 8, 256);
+    return p;
+}
+
 }  // namespace w4

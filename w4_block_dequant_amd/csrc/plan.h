@@ -118,4 +118,13 @@ int64_t kv_attend_units(int64_t seqs, int64_t q_heads, int64_t heads, int64_t ma
 KvAttendPlan plan_kv_attend(int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim,
                             int64_t max_len, bool weigh);
 
+// ---- log probabilities -----------------------------------------------------------
+// A row is cut into `chunks` pieces of `chunk` logits where there are few rows.
+struct LogprobsPlan {
+    int64_t chunks = 1, chunk = 0;
+    size_t keys = 0, workspace = 0;
+};
+
+LogprobsPlan plan_logprobs(int64_t M, int64_t N, int64_t top);
+
 }  // namespace w4
