@@ -1,26 +1,64 @@
 // Append of new keys and values to the paged cache, with the conversion to the
 // cache's type (see kv.h and include/w4.h).
 //
-// One workgroup takes one (row, head): its two rows of head_dim fp32 values
-// are read once and stored converted.  KV_I8 needs the row's largest magnitude
-// before the first code.
+// Bound: the rows' bytes read and written; a decode step's few rows, the launch.
+// A group of lanes (a power of two, 8 values to a lane) takes one (row, head):
+// it finds the row's place once for both its keys and its values, reads 32 bytes
+// of each in a lane and stores 8 values converted (16 bytes of a 16-bit cache).
+// KV_I8 forms the largest magnitude of a row over the group's lanes first.
 #include "kv.h"
 #include "launch.h"
 
 namespace w4 {
 namespace {
 
+typedef float f32x4u_t __attribute__((ext_vector_type(4), aligned(4)));
+
+// Eight values as the cache's type holds them (not KV_I8).
 template <int DT>
-__global__ __launch_bounds__(64) void k_kv_append(KvPool c, const float *k, int64_t k_stride,
-                                                  const float *v, int64_t v_stride,
-                                                  const int32_t *table, int64_t seqs,
-                                                  int64_t cols, const int32_t *seq,
-                                                  const int32_t *at, int *d_status) {
-    const int64_t r = blockIdx.x / c.heads;
-    const int h = (int)(blockIdx.x % c.heads);
-    const int lane = threadIdx.x;
+__device__ __forceinline__ void put8(void *pool, int64_t at, const float *f) {
+    using T = typename KvType<DT>::T;
+    if constexpr (DT == KV_F32) {
+        f32x4_t *to = (f32x4_t *)((T *)pool + at);
+        to[0] = f32x4_t{f[0], f[1], f[2], f[3]};
+        to[1] = f32x4_t{f[4], f[5], f[6], f[7]};
+    } else {
+        u32x4_t w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = (uint32_t)KvType<DT>::put(f[2 * i]) |
+                   (uint32_t)KvType<DT>::put(f[2 * i + 1]) << 16;
+        *(u32x4_t *)((T *)pool + at) = w;
+    }
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void k_kv_append(const float *__restrict__ k,
+                                                   const float *__restrict__ v,
+                                                   const int32_t *__restrict__ seq,
+                                                   const int32_t *__restrict__ at,
+                                                   const int32_t *__restrict__ table,
+                                                   int64_t k_stride, int64_t v_stride,
+                                                   int64_t rows, int64_t seqs, int64_t cols,
+                                                   int group_bits, KvPool c, int *d_status) {
+    const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> group_bits;
+    const int64_t r = item / c.heads;
+    if (r >= rows) return;
+    const int h = (int)(item - r * c.heads);
+    const int x = threadIdx.x & ((1 << group_bits) - 1);  // the lane within its group
+    // lanes past head_dim repeat the last one's work and store nothing
+    const bool mine = 8 * x < c.dim;
+    const int64_t from = (int64_t)h * c.dim + min(8 * x, c.dim - 8);
+    float f[2][8];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const f32x4u_t *p = (const f32x4u_t *)((w ? v + r * v_stride : k + r * k_stride) + from);
+        const f32x4_t a = p[0], b = p[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[w][i] = a[i], f[w][4 + i] = b[i];
+    }
     const int s = seq[r], t = at[r];
-    if (s < 0) return;
+    if (s < 0) return;  // padding
     if (s >= seqs || t < 0 || (t >> c.shift) >= cols) {
         set_status(d_status, W4_ERR_BAD_SHAPE);
         return;
@@ -31,29 +69,39 @@ __global__ __launch_bounds__(64) void k_kv_append(KvPool c, const float *k, int6
         return;
     }
     const int64_t row = kv_row(c, page, h, t & ((1 << c.shift) - 1));
-    if (c.weight && lane == 0) c.weight[row] = 0.0f;
-    for (int w = 0; w < 2; ++w) {
-        const float *x = (w ? v + r * v_stride : k + r * k_stride) + (int64_t)h * c.dim;
-        void *pool = w ? c.v : c.k;
-        if constexpr (DT == KV_I8) {
-            float m = 0.0f;
-            bool bad = false;
-            for (int d = lane; d < c.dim; d += 64) {
-                m = fmaxf(m, fabsf(x[d]));
-                bad |= !isfinite(x[d]);
-            }
-            for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-            if (bad) set_status(d_status, W4_ERR_NONFINITE);
-            const float scale = m / 127.0f;
-            for (int d = lane; d < c.dim; d += 64) {
-                const float q = scale == 0.0f ? 0.0f : rintf(x[d] / scale);
-                ((int8_t *)pool)[row * c.dim + d] = (int8_t)fminf(fmaxf(q, -127.0f), 127.0f);
-            }
-            if (lane == 0) (w ? c.v_scale : c.k_scale)[row] = scale;
-        } else {
-            for (int d = lane; d < c.dim; d += 64)
-                ((typename KvType<DT>::T *)pool)[row * c.dim + d] = KvType<DT>::put(x[d]);
+    const int64_t to = row * c.dim + 8 * x;
+    if (c.weight && x == 0) c.weight[row] = 0.0f;
+    if constexpr (DT == KV_I8) {
+        // the largest magnitude as bits: a non-finite value gives the largest of all
+        float scale[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                top = max(top, __builtin_bit_cast(uint32_t, f[w][i]) & 0x7FFFFFFFu);
+            for (int o = (1 << group_bits) >> 1; o > 0; o >>= 1)
+                top = max(top, (uint32_t)__shfl_xor((int)top, o));
+            if (top >= 0x7F800000u) set_status(d_status, W4_ERR_NONFINITE);
+            scale[w] = __builtin_bit_cast(float, top) / 127.0f;
         }
+        if (x == 0) c.k_scale[row] = scale[0], c.v_scale[row] = scale[1];
+        if (mine) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                uint32_t word[2] = {0, 0};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float q = scale[w] == 0.0f ? 0.0f : rintf(f[w][i] / scale[w]);
+                    const int code = (int)fminf(fmaxf(q, -127.0f), 127.0f);
+                    word[i / 4] |= (uint32_t)(code & 0xFF) << (8 * (i % 4));
+                }
+                *(u32x2_t *)((int8_t *)(w ? c.v : c.k) + to) = u32x2_t{word[0], word[1]};
+            }
+        }
+    } else if (mine) {
+        put8<DT>(c.k, to, f[0]);
+        put8<DT>(c.v, to, f[1]);
     }
 }
 
@@ -63,10 +111,13 @@ hipError_t launch_kv_append(const KvPool &c, int dtype, const float *k, int64_t 
                             const float *v, int64_t v_stride, int64_t rows, const int32_t *table,
                             int64_t seqs, int64_t cols, const int32_t *seq, const int32_t *at,
                             int *d_status, hipStream_t stream) {
-    const dim3 grid((unsigned)(rows * c.heads));
+    int group_bits = 0;
+    while (8 << group_bits < c.dim) ++group_bits;
+    const int64_t groups = (((rows * c.heads) << group_bits) + 255) / 256;
+    if (groups > 0x7FFFFFFF) return hipErrorInvalidValue;
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, dim3(64), 0, stream, c, k, k_stride, v, v_stride, table,
-                           seqs, cols, seq, at, d_status);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(256), 0, stream, k, v, seq, at,
+                           table, k_stride, v_stride, rows, seqs, cols, group_bits, c, d_status);
         return hipGetLastError();
     };
     switch (dtype) {
