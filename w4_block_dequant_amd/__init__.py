@@ -142,7 +142,10 @@ def _ptr(t):
 
 
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the handle of torch.cuda.current_stream(device), without building a Stream object (2 us)
+    index = device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None
+                                              else index)
 
 
 class Workspace:
@@ -164,7 +167,8 @@ class Workspace:
     def get(self, device, nbytes: int):
         if nbytes == 0:
             return None, 0
-        key = (torch.device(device).index, _stream(device))
+        device = torch.device(device)
+        key = (device.index, _stream(device))
         with self._lock:
             buf = self._buf.get(key)
             if buf is None or buf.numel() < nbytes:
@@ -621,12 +625,13 @@ class KvCache(ctypes.Structure):
 def _kv_cache(K, V, k_scale, v_scale, weight) -> KvCache:
     if not isinstance(K, torch.Tensor) or K.dtype not in KV_DTYPES:
         raise TypeError("K must be a float32, float16, bfloat16 or int8 tensor")
-    _dev(K, K.dtype, "K")
-    _dev(V, K.dtype, "V")
+    dtype = K.dtype
+    _dev(K, dtype, "K")
+    _dev(V, dtype, "V")
     shape = K.shape
     if len(shape) != 4 or V.shape != shape:
         raise ValueError("K and V must be [pages, heads, page_size, head_dim], of one shape")
-    if K.dtype == torch.int8:
+    if dtype == torch.int8:
         if k_scale is None or v_scale is None:
             raise ValueError("an int8 cache needs k_scale and v_scale")
         _dev(k_scale, torch.float32, "k_scale")
@@ -639,31 +644,40 @@ def _kv_cache(K, V, k_scale, v_scale, weight) -> KvCache:
         _dev(weight, torch.float32, "weight")
         if weight.shape != shape[:3]:
             raise ValueError("weight must be [pages, heads, page_size]")
-    return KvCache(_ptr(K), _ptr(V), _ptr(k_scale), _ptr(v_scale), _ptr(weight), *shape,
-                   KV_DTYPES[K.dtype])
+    return KvCache(K.data_ptr(), V.data_ptr(), _ptr(k_scale), _ptr(v_scale), _ptr(weight), *shape,
+                   KV_DTYPES[dtype])
 
 
-def _kv_ints(t, name, shape):
-    """An int32 device tensor of the given shape (None: any)."""
+def _kv_ints(t, name, *shape):
+    """An int32 device tensor of the given shape."""
     _dev(t, torch.int32, name)
-    if t.dim() != len(shape) or any(n is not None and m != n for m, n in zip(t.shape, shape)):
+    if t.shape != shape:
         raise ValueError(f"{name} must be int32 {list(shape)}, got {list(t.shape)}")
-    return t
+
+
+def _kv_table(t, name, seqs=None):
+    """An int32 device table [seqs, columns] (None: of any number of sequences); its shape."""
+    _dev(t, torch.int32, name)
+    shape = t.shape
+    if len(shape) != 2 or (seqs is not None and shape[0] != seqs):
+        raise ValueError(f"{name} must be int32 [sequences, columns], got {list(shape)}")
+    return shape
 
 
 def _kv_rows(t, name, width):
-    """fp32 [rows, heads, dim] whose rows are dense but may lie apart; (heads, row stride)."""
+    """fp32 [rows, heads, width] whose rows are dense but may lie apart: (rows, heads, row stride)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a tensor on a HIP device")
     if t.dtype != torch.float32:
         raise TypeError(f"{name} must be float32, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != width:
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != width:
         raise ValueError(f"{name} must be [rows, heads, {width}]")
-    rows, heads, _ = t.shape
+    rows, heads, _ = shape
     stride = t.stride()
     if stride[2] != 1 or (heads > 1 and stride[1] != width):
         raise ValueError(f"{name}: a row's heads must be contiguous")
-    return heads, (stride[0] if rows > 1 else heads * width)
+    return rows, heads, (stride[0] if rows > 1 else heads * width)
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
@@ -675,18 +689,17 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, K: torch.Tensor, V: torch.Tensor
     (fp32, fp16, bf16; int8 with scales fp32 [pages, heads, page_size]).  table int32
     [sequences, columns], seq and at int32 [rows]; weight becomes 0 at the stored positions."""
     cache = _kv_cache(K, V, k_scale, v_scale, weight)
-    heads, ks = _kv_rows(k, "k", cache.head_dim)
-    heads_v, vs = _kv_rows(v, "v", cache.head_dim)
-    rows = k.shape[0]
-    if heads != cache.heads or heads_v != heads or v.shape[0] != rows:
+    rows, heads, ks = _kv_rows(k, "k", cache.head_dim)
+    rows_v, heads_v, vs = _kv_rows(v, "v", cache.head_dim)
+    if heads != cache.heads or heads_v != heads or rows_v != rows:
         raise ValueError("k and v must be [rows, heads, head_dim] with the cache's heads")
-    _kv_ints(table, "table", (None, None))
-    _kv_ints(seq, "seq", (rows,))
-    _kv_ints(at, "at", (rows,))
+    seqs, cols = _kv_table(table, "table")
+    _kv_ints(seq, "seq", rows)
+    _kv_ints(at, "at", rows)
     if d_status is not None:
         _dev(d_status, torch.int32, "d_status")
     _check("kv_append", _lib.kv_append(
-        ctypes.byref(cache), _ptr(k), ks, _ptr(v), vs, rows, _ptr(table), *table.shape, _ptr(seq),
+        ctypes.byref(cache), _ptr(k), ks, _ptr(v), vs, rows, _ptr(table), seqs, cols, _ptr(seq),
         _ptr(at), _ptr(d_status), _stream(K.device)))
 
 
@@ -703,12 +716,11 @@ def kv_attend(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, table: torch.Te
     the table holds); it sets how the length is split.  weight: if given, grows by the attention
     that each position takes."""
     cache = _kv_cache(K, V, k_scale, v_scale, weight)
-    q_heads, qs = _kv_rows(q, "q", cache.head_dim)
-    seqs = q.shape[0]
-    _kv_ints(table, "table", (seqs, None))
-    _kv_ints(lens, "lens", (seqs,))
+    seqs, q_heads, qs = _kv_rows(q, "q", cache.head_dim)
+    _, cols = _kv_table(table, "table", seqs)
+    _kv_ints(lens, "lens", seqs)
     if starts is not None:
-        _kv_ints(starts, "starts", (seqs,))
+        _kv_ints(starts, "starts", seqs)
     if d_status is not None:
         _dev(d_status, torch.int32, "d_status")
     if out is None:
@@ -717,7 +729,6 @@ def kv_attend(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, table: torch.Te
         _dev(out, torch.float32, "out")
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
-    cols = table.shape[1]
     if workspace is None:
         most = cols * cache.page_size
         need = _lib.kv_attend_workspace_bytes(ctypes.byref(cache), seqs, q_heads,
@@ -747,21 +758,20 @@ def kv_evict(K: torch.Tensor, V: torch.Tensor, weight: torch.Tensor, table: torc
     if weight is None:
         raise ValueError("eviction goes by weight")
     cache = _kv_cache(K, V, k_scale, v_scale, weight)
-    _kv_ints(table, "table", (None, None))
-    seqs, cols = table.shape
-    _kv_ints(lens, "lens", (seqs,))
-    _kv_ints(table_out, "table_out", (seqs, None))
+    seqs, cols = _kv_table(table, "table")
+    _kv_ints(lens, "lens", seqs)
+    _, cols_out = _kv_table(table_out, "table_out", seqs)
     if kept is None:
         kept = torch.empty((seqs, cache.heads, max(keep, 0)), dtype=torch.int32, device=K.device)
     if lens_out is None:
         lens_out = torch.empty(seqs, dtype=torch.int32, device=K.device)
-    _kv_ints(kept, "kept", (seqs, cache.heads, keep))
-    _kv_ints(lens_out, "lens_out", (seqs,))
+    _kv_ints(kept, "kept", seqs, cache.heads, keep)
+    _kv_ints(lens_out, "lens_out", seqs)
     if d_status is not None:
         _dev(d_status, torch.int32, "d_status")
     _check("kv_evict", _lib.kv_evict(
         ctypes.byref(cache), _ptr(table), seqs, cols, _ptr(lens), max_len, keep, recent,
-        _ptr(table_out), table_out.shape[1], _ptr(kept), _ptr(lens_out), _ptr(d_status),
+        _ptr(table_out), cols_out, _ptr(kept), _ptr(lens_out), _ptr(d_status),
         _stream(K.device)))
     return kept, lens_out
 
