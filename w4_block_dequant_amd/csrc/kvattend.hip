@@ -38,10 +38,11 @@
 //
 // Operands are exact or as good as fp32, sums are fp32 (the matrix cores'):
 //   bf16 cache: q and p are split exactly into three bf16 terms.
-//   int8 cache: codes are exact in bf16; the scales multiply s and p in fp32.
 //   fp16 cache: q (scaled by a power of two to [2^14, 2^15)) and p (in units of
 //     2^-15) are split into two fp16 terms, h = fp16(a) and fp16(a - h): 2^-24
 //     relative, 2^-40 of the row's largest absolute.
+//   int8 cache: codes are exact in fp16 and in bf16; q as for fp16, p times the
+//     value's scale as for bf16; the key's scale multiplies s in fp32.
 //   fp32 cache: v_mfma_f32_16x16x4_f32, one k step for each of a lane's 8 dims.
 // Scores are in units of log2(e): p = exp2(s - m).  Positions outside the
 // range get s = -infinity by selection and values of zero, whatever their
@@ -78,31 +79,45 @@ __device__ __forceinline__ float pow2(float v) { return __builtin_amdgcn_exp2f(v
 __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
     return (uint32_t)f32_to_f16_bits(a) | (uint32_t)f32_to_f16_bits(b) << 16;
 }
-// Element i (0..3) of four signed codes, as fp32.
+// Signed codes as fp16, exactly, two to a word: 0x6400 | (code + 128) is the
+// fp16 number 1024 + 128 + code, so one permutation, one flip of the sign bits
+// and one packed subtraction do it, where converting takes an instruction of a
+// quarter of the rate for each code.
+__device__ __forceinline__ uint32_t code_pair(uint32_t magic) {
+    const half2_t v = as_half2(magic) + half2_t{(_Float16)-1152.0f, (_Float16)-1152.0f};
+    return __builtin_bit_cast(uint32_t, v);
+}
+// Codes 2 i and 2 i + 1 (i = 0, 1) of a word whose sign bits are flipped.
+__device__ __forceinline__ uint32_t codes_along(uint32_t flipped, int i) {
+    return code_pair(__builtin_amdgcn_perm(0x64646464u, flipped, i ? 0x04030402u : 0x04010400u));
+}
+// Element i (0..3) of four signed codes, as fp32 (whose upper half is its bf16).
 __device__ __forceinline__ float code_at(uint32_t w, int i) {
     return (float)(int)(int8_t)(w >> (8 * i));
 }
 
-// PARTS: terms that q and p are split into; operand words (of 8 elements).
+// The matrix operands of a product: fp32 as it is, three bf16 terms, or two fp16
+// terms.
+enum Operands { kPlain, kThreeBf16, kTwoHalf };
 template <int DT>
-struct Parts {
-    static constexpr int n = DT == KV_F16 ? 2 : 3;
-};
-template <>
-struct Parts<KV_F32> {
-    static constexpr int n = 1;
-};
+constexpr Operands kOfScores = DT == KV_F32    ? kPlain
+                               : DT == KV_BF16 ? kThreeBf16
+                                               : kTwoHalf;
+template <int DT>
+constexpr Operands kOfOutput = DT == KV_F32 ? kPlain : DT == KV_F16 ? kTwoHalf : kThreeBf16;
+// p in units of 2^-15 where it is split into fp16 terms
+constexpr float kHalfUnit = 32768.0f;
 
-// Eight fp32 values as matrix operands: 4 words for each term (fp32: as they are).
-template <int DT>
+// Eight fp32 values as operands: 4 words for each term (fp32: 8 words).
+template <Operands OP>
 struct Split {
-    static constexpr int words = DT == KV_F32 ? 8 : 4;
-    uint32_t w[Parts<DT>::n][words];
+    static constexpr int terms = OP == kPlain ? 1 : OP == kThreeBf16 ? 3 : 2;
+    uint32_t w[terms][OP == kPlain ? 8 : 4];
     __device__ __forceinline__ void set(const float *f) {
-        if constexpr (DT == KV_F32) {
+        if constexpr (OP == kPlain) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[0][i] = fbits(f[i]);
-        } else if constexpr (DT == KV_F16) {
+        } else if constexpr (OP == kTwoHalf) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float a = f[2 * i], b = f[2 * i + 1];
@@ -123,9 +138,9 @@ struct Split {
     }
 };
 
-template <int DT>
+template <Operands OP>
 __device__ __forceinline__ f32x4_t mfma8(const uint32_t *a, const uint32_t *b, f32x4_t c) {
-    if constexpr (DT == KV_F32) {
+    if constexpr (OP == kPlain) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             c = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, a[e]),
@@ -133,7 +148,7 @@ __device__ __forceinline__ f32x4_t mfma8(const uint32_t *a, const uint32_t *b, f
         return c;
     } else {
         const u32x4_t av = {a[0], a[1], a[2], a[3]}, bv = {b[0], b[1], b[2], b[3]};
-        if constexpr (DT == KV_F16)
+        if constexpr (OP == kTwoHalf)
             return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, av),
                                                           __builtin_bit_cast(f16x8_t, bv), c, 0, 0,
                                                           0);
@@ -147,33 +162,36 @@ __device__ __forceinline__ f32x4_t mfma8(const uint32_t *a, const uint32_t *b, f
 template <int DT>
 constexpr int kElem = DT == KV_F32 ? 4 : DT == KV_I8 ? 1 : 2;
 
-// N consecutive elements from p (N * size bytes, aligned to their number of
-// bytes or 16), as words.
-template <int BYTES>
+// BYTES from p, as words.  NT: read once, not to be kept in the caches.
+template <bool NT, class T>
+__device__ __forceinline__ T load_as(const char *p) {
+    return NT ? load_stream<T>(p) : *(const T *)p;
+}
+template <int BYTES, bool NT>
 __device__ __forceinline__ void load_words(const char *p, uint32_t *w) {
     if constexpr (BYTES == 4) {
-        w[0] = load_stream<uint32_t>(p);
+        w[0] = load_as<NT, uint32_t>(p);
     } else if constexpr (BYTES == 8) {
-        const u32x2_t v = load_stream<u32x2_t>(p);
+        const u32x2_t v = load_as<NT, u32x2_t>(p);
         w[0] = v.x;
         w[1] = v.y;
     } else {
 #pragma unroll
         for (int i = 0; i < BYTES / 16; ++i) {
-            const u32x4_t v = load_stream<u32x4_t>(p + 16 * i);
+            const u32x4_t v = load_as<NT, u32x4_t>(p + 16 * i);
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
         }
     }
 }
 
-// Where the two 16-position halves of a tile lie.  No padding: the compiler
-// copies padding through memory, puts that into LDS, and then reads the
-// workgroup's size from the dispatch packet in host memory, 15 us for a grid
-// of 2000 waves.
+// Where the 16-position groups of a tile lie.  No padding: the compiler copies
+// padding through memory, puts that into LDS, and then reads the workgroup's
+// size from the dispatch packet in host memory, 15 us for a grid of 2000 waves.
+template <int H>
 struct TilePages {
-    int64_t row0, row1;  // pool row of the half's first position
-    int ok0, ok1;
+    int64_t row[H];  // pool row of the group's first position
+    int ok[H];       // its page is one of the pool's
 };
 
 // Sums over a wave in six additions: every lane's sum of itself and the lanes
@@ -194,17 +212,21 @@ __device__ __forceinline__ int wave_sum(int v) {
     return __builtin_amdgcn_readlane(wave_scan(v), 63);
 }
 
-// Steps of one sequence: 128 positions each, from the tile that holds lo on.
-constexpr int kStep = 128;
-__device__ __forceinline__ int kv_steps(int lo, int n) {
-    return n > lo ? (n - (lo & ~31) + kStep - 1) / kStep : 0;
-}
+constexpr int kTile = 32;             // positions of a wave's tile
+constexpr int kStep = kTile * kWaves;  // of a workgroup's step, one unit of the list
 // Units that a block counts beside its steps, before them: what its start and
-// end cost a workgroup.
+// end cost a workgroup (1, 2, 4: 31 ragged sequences with weights 71, 69, 70 us).
 constexpr int kOpen = kKvOpenUnits;
-constexpr int kPart = kKvPartSteps;  // the least steps of a part
-__device__ __forceinline__ int kv_units(int steps, int part) {
-    return part ? max(1, (steps + part - 1) / part) : steps + kOpen;
+// The least steps of a part (2, 3, 4, 8: one sequence of 32 x 96 at 4095
+// positions 21, 23, 19, 23 us).
+constexpr int kPart = kKvPartSteps;
+// Steps from the tile that holds position lo on.
+__device__ __forceinline__ int kv_begin(int lo) { return lo & ~(kTile - 1); }
+__device__ __forceinline__ int kv_steps(int lo, int n) {
+    return n > lo ? (n - kv_begin(lo) + kStep - 1) / kStep : 0;
+}
+__device__ __forceinline__ int kv_units(int steps, int cut) {
+    return cut ? max(1, (steps + cut - 1) / cut) : steps + kOpen;
 }
 
 // What the first kernel leaves for the second, in the workspace.
@@ -217,8 +239,11 @@ struct KvParts {
     int64_t score_stride;
 };
 
-// NB: blocks of 32 dims of a query; DL: dims of the values that a lane owns.
-template <int DT, int NB, int DL>
+// NB: blocks of 32 dims of a query; DL: dims of the values that a lane owns;
+// PAIR: int8 keys are read 16 codes to a lane, 64 dims (64 bytes of a row) to an
+// instruction, so that no cache line's half is asked for twice: lane c's two
+// blocks hold dims 64 i + 16 c .. + 15.  Needs head_dim >= 16.
+template <int DT, int NB, int DL, bool PAIR = false>
 __global__ __launch_bounds__(64 * kWaves) void k_kv_attend(
     const float *__restrict__ q, const int32_t *__restrict__ table,
     const int32_t *__restrict__ lens, const int32_t *__restrict__ starts, int seqs, int q_heads,
@@ -226,10 +251,19 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attend(
     int *d_status) {
     constexpr int ES = kElem<DT>;
     constexpr int KW = 8 * ES / 4;           // words of a lane's 8 key dims
-    constexpr int DC = DL < 8 ? DL : 8;      // dims of one chunk of a lane's values
+    // a lane's value dims come in NC chunks, chunk k at (16 k + x) DC: 16 bytes each
+    // (fewer of a small head), so that an instruction reads whole lines of a row
+    constexpr int DC = DT == KV_F32 ? 4 : DL < 8 ? DL : 8;
     constexpr int NC = DL / DC;              // chunks
     constexpr int VW = DC * ES / 4;          // words of a chunk
-    constexpr int P = Parts<DT>::n;
+    constexpr Operands QK = kOfScores<DT>, PV = kOfOutput<DT>;
+    // Streaming loads, except of int8 rows of up to 96 bytes: those end within a
+    // 64-byte line, whose other part another instruction reads (16 ragged
+    // sequences of 32 x 96: 54.6 us streaming, 51.8 not; whole lines, 4 x 131072
+    // positions of 8 x 128 bf16: 319 against 356)
+    constexpr bool NT = !(DT == KV_I8 && NB == 3);
+    constexpr int H = kTile / 16;            // 16-position groups of a tile
+    constexpr int NP = 4 * H;                // positions of a lane in a tile
     __shared__ float s_m[kWaves][16], s_l[kWaves][16];
     __shared__ float s_acc[kWaves][16][NC * 16 * DC + 4];
 
@@ -257,8 +291,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attend(
         const uint32_t steps = (uint32_t)wave_sum(sum) * blocks;
         total = steps + (uint32_t)seqs * blocks * kOpen;
         if ((uint32_t)seqs * blocks <= gridDim.x) {
-            const uint32_t even = steps / gridDim.x;
-            for (uint32_t s = max(even, (uint32_t)kPart); s <= max(even, (uint32_t)kPart) + 2; ++s) {
+            const uint32_t least = max(steps / gridDim.x, (uint32_t)kPart);
+            for (uint32_t s = least; s <= least + 2; ++s) {
                 int count = lane < seqs ? max(1, (mine + (int)s - 1) / (int)s) : 0;
                 for (int i = lane + 64; i < seqs; i += 64)
                     count += max(1, (steps_of(i) + (int)s - 1) / (int)s);
@@ -293,14 +327,35 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attend(
     const int row_bytes = c.dim * ES;
     // dims past head_dim read the row's start: their q is zero, their outputs
     // are not stored
-    int koff[NB];
+    constexpr int PAIRS = PAIR ? NB / 2 : 0;
+    // the dims of elements 4 half .. + 3 of a lane's eight of block k, or -1
+    auto dim_of = [&](int k, int half) {
+        if (k < 2 * PAIRS) {
+            // where a row ends within the 16 codes, they are read 8 earlier: the
+            // first half then counts nothing, being another lane's
+            const int d = 64 * (k / 2) + 16 * cg;
+            if (d + 16 <= c.dim) return d + 8 * (k % 2) + 4 * half;
+            return d + 8 == c.dim && k % 2 ? d + 4 * half : -1;
+        }
+        // fp32: 16 bytes of 64, twice
+        const int d = DT == KV_F32 ? 32 * k + 16 * half + 4 * cg : 32 * k + 8 * cg + 4 * half;
+        return d < c.dim ? d : -1;
+    };
+    constexpr int KL = DT == KV_F32 ? 2 : 1;  // loads of a block
+    int koff[NB * KL];
 #pragma unroll
-    for (int k = 0; k < NB; ++k)
-        koff[k] = x * row_bytes + (32 * k + 8 * cg < c.dim ? (32 * k + 8 * cg) * ES : 0);
+    for (int k = 0; k < NB * KL; ++k) {
+        int d = dim_of(k / KL, k % KL);
+        if (k < 2 * PAIRS) {
+            d = 64 * (k / 2) + 16 * cg;
+            d = d + 16 <= c.dim ? d : d + 8 == c.dim ? d - 8 : 0;
+        }
+        koff[k] = x * row_bytes + max(d, 0) * ES;
+    }
     int voff[NC];
 #pragma unroll
     for (int k = 0; k < NC; ++k)
-        voff[k] = 4 * cg * row_bytes + (x * DL + k * DC < c.dim ? (x * DL + k * DC) * ES : 0);
+        voff[k] = 4 * cg * row_bytes + ((16 * k + x) * DC < c.dim ? (16 * k + x) * DC * ES : 0);
 
     int n = kv_length(lens, b, most, d_status), lo = first_of(b), steps = kv_steps(lo, n);
     for (int u = u0; u < u1;) {
@@ -313,7 +368,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attend(
     const int to = part ? min((u - start + 1) * even, steps) : stop - start - kOpen;
     const int h = vb / gblocks, g0 = vb % gblocks * 16, gn = min(16, G - g0);
     const int hq0 = h * G + g0;
-    const int first = (lo & ~31) + from * kStep, last = min((lo & ~31) + to * kStep, n);
+    const int first = kv_begin(lo) + from * kStep;
+    const int last = min(kv_begin(lo) + to * kStep, n);
     const int32_t *tab = table + (int64_t)b * cols;
     const bool whole_block = from == 0 && to == steps;
     if (parts.owner && u == start && threadIdx.x == 0) {
@@ -326,46 +382,58 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attend(
     if (to > from) {
 
     auto find = [&](int t0) {
-        TilePages p;
-        const int e0 = t0 >> c.shift, e1 = (t0 + 16) >> c.shift;
-        const int p0 = tab[e0];
-        const int p1 = e1 == e0 || t0 + 16 >= last ? p0 : tab[e1];
-        p.ok0 = kv_page_ok(c, p0);
-        p.ok1 = kv_page_ok(c, p1);
-        if (!p.ok0 || !p.ok1) set_status(d_status, W4_ERR_BAD_SHAPE);
-        p.row0 = kv_row(c, p.ok0 ? p0 : 0, h, t0 & mask);
-        p.row1 = kv_row(c, p.ok1 ? p1 : 0, h, (t0 + 16) & mask);
+        TilePages<H> p;
+#pragma unroll
+        for (int u = 0; u < H; ++u) {
+            // groups past the end read its page, and no entry past it
+            const int t = t0 + 16 * u;
+            const int page = tab[min(t, last - 1) >> c.shift];
+            p.ok[u] = kv_page_ok(c, page);
+            if (!p.ok[u]) set_status(d_status, W4_ERR_BAD_SHAPE);
+            p.row[u] = kv_row(c, p.ok[u] ? page : 0, h, t & mask);
+        }
         return p;
     };
 
-    uint32_t kw[2][NB][KW];
-    uint32_t vw[8][NC][VW];
-    f32x4_t ksc[2], vsc[2];
-    auto load_keys = [&](const TilePages &p) {
+    // `live` 0: every lane reads the group's first bytes (a load that nothing
+    // uses costs a cache line then, and no branch)
+    uint32_t kw[H][NB][KW];
+    uint32_t vw[NP][NC][VW];
+    f32x4_t ksc[H], vsc[H];
+    auto load_keys = [&](const TilePages<H> &p, int live) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int64_t row = u ? p.row1 : p.row0;
-            const char *base = (const char *)c.k + row * row_bytes;
+        for (int u = 0; u < H; ++u) {
+            const char *base = (const char *)c.k + p.row[u] * row_bytes;
 #pragma unroll
-            for (int k = 0; k < NB; ++k) load_words<8 * ES>(base + koff[k], kw[u][k]);
-            if constexpr (DT == KV_I8) {
-                ksc[u] = *(const f32x4u_t *)(c.k_scale + row + 4 * cg);
+            for (int k = 0; k < NB; ++k) {
+                if (k >= 2 * PAIRS) {
+#pragma unroll
+                    for (int i = 0; i < KL; ++i)
+                        load_words<8 * ES / KL, NT>(base + (koff[k * KL + i] & live),
+                                                kw[u][k] + i * KW / KL);
+                } else if (k % 2 == 0) {
+                    uint32_t w[4];
+                    load_words<16, NT>(base + (koff[k] & live), w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kw[u][k + i / 2][i % 2] = w[i];
+                }
             }
+            if constexpr (DT == KV_I8)
+                ksc[u] = *(const f32x4u_t *)(c.k_scale + p.row[u] + 4 * cg);
         }
     };
-    auto load_values = [&](const TilePages &p) {
+    auto load_values = [&](const TilePages<H> &p, int live) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int64_t row = u ? p.row1 : p.row0;
-            const char *base = (const char *)c.v + row * row_bytes;
+        for (int u = 0; u < H; ++u) {
+            const char *base = (const char *)c.v + p.row[u] * row_bytes;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int k = 0; k < NC; ++k)
-                    load_words<DC * ES>(base + voff[k] + j * row_bytes, vw[4 * u + j][k]);
-            if constexpr (DT == KV_I8) {
-                vsc[u] = *(const f32x4u_t *)(c.v_scale + row + 4 * cg);
-            }
+                    load_words<DC * ES, NT>(base + (voff[k] & live) + j * row_bytes,
+                                        vw[4 * u + j][k]);
+            if constexpr (DT == KV_I8)
+                vsc[u] = *(const f32x4u_t *)(c.v_scale + p.row[u] + 4 * cg);
         }
     };
 
@@ -375,13 +443,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attend(
 #pragma unroll
     for (int e = 0; e < NC * DC; ++e) acc[e] = zero4;
 
-    int t0 = first + 32 * wave;
+    int t0 = first + kTile * wave;
     if (t0 < last) {
-        TilePages pg = find(t0);
-        load_keys(pg);
-        load_values(pg);
+        TilePages<H> pg = find(t0);
+        load_keys(pg, -1);
+        load_values(pg, -1);
         // queries: column x of the B operands, all blocks
-        Split<DT> qs[NB];
+        Split<QK> qs[NB];
         float sc = scale * 1.4426950408889634f;
         {
             float f[NB][8];
@@ -389,14 +457,16 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attend(
             const float *qp = q + (int64_t)b * q_stride + (int64_t)(hq0 + min(x, gn - 1)) * c.dim;
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
-                const int d0 = 32 * k + 8 * cg;
-                const bool in = x < gn && d0 < c.dim;
-                const f32x4u_t *at = (const f32x4u_t *)(qp + (d0 < c.dim ? d0 : 0));
-                const f32x4_t v0 = at[0], v1 = at[1];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[k][e] = in ? v0[e] : 0.0f, f[k][4 + e] = in ? v1[e] : 0.0f;
+                for (int half = 0; half < 2; ++half) {
+                    const int d = dim_of(k, half);
+                    const f32x4_t v = *(const f32x4u_t *)(qp + max(d, 0));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        f[k][4 * half + e] = x < gn && d >= 0 ? v[e] : 0.0f;
+                }
             }
-            if constexpr (DT == KV_F16) {
+            if constexpr (QK == kTwoHalf) {
                 float top = 0.0f;
 #pragma unroll
                 for (int k = 0; k < NB; ++k)
@@ -415,44 +485,48 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attend(
 #pragma unroll
             for (int k = 0; k < NB; ++k) qs[k].set(f[k]);
         }
-        for (; t0 < last; t0 += 32 * kWaves) {
+        for (; t0 < last; t0 += kStep) {
             // the next tile's loads go out as soon as this tile has used its own
-            // (past the end: this tile's again, so that nothing depends on a branch)
-            const TilePages next = t0 + 32 * kWaves < last ? find(t0 + 32 * kWaves) : pg;
-            f32x4_t s[2] = {zero4, zero4};
+            const bool more = t0 + kStep < last;
+            const TilePages<H> next = find(more ? t0 + kStep : t0);
+            f32x4_t s[H];
+#pragma unroll
+            for (int u = 0; u < H; ++u) s[u] = zero4;
 #pragma unroll
             for (int k = 0; k < NB; ++k)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < H; ++u) {
                     uint32_t a[8];
                     if constexpr (DT == KV_I8) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            a[i] = hi16_pair(fbits(code_at(kw[u][k][i / 2], 2 * (i & 1))),
-                                             fbits(code_at(kw[u][k][i / 2], 2 * (i & 1) + 1)));
+                            a[i] = codes_along(kw[u][k][i / 2] ^ 0x80808080u, i & 1);
                     } else {
 #pragma unroll
                         for (int i = 0; i < KW; ++i) a[i] = kw[u][k][i];
                     }
 #pragma unroll
-                    for (int r = P - 1; r >= 0; --r) s[u] = mfma8<DT>(a, qs[k].w[r], s[u]);
+                    for (int r = Split<QK>::terms - 1; r >= 0; --r)
+                        s[u] = mfma8<QK>(a, qs[k].w[r], s[u]);
                 }
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < H; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     s[u][i] *= sc;
                     if constexpr (DT == KV_I8) s[u][i] *= ksc[u][i];
                 }
-            load_keys(next);
-            const bool whole = t0 >= lo && t0 + 32 <= last && pg.ok0 && pg.ok1;
+            load_keys(next, more ? -1 : 0);
+            bool whole = t0 >= lo && t0 + kTile <= last;
+#pragma unroll
+            for (int u = 0; u < H; ++u) whole = whole && pg.ok[u];
             // bit 4 u + i: this lane's position takes part
-            uint32_t in = 0xFFu;
+            uint32_t in = (1u << NP) - 1;
             if (!whole) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < NP; ++i) {
                     const int t = t0 + 16 * (i / 4) + 4 * cg + i % 4;
-                    if (t < lo || t >= last || !(i < 4 ? pg.ok0 : pg.ok1)) {
+                    if (t < lo || t >= last || !pg.ok[i / 4]) {
                         in &= ~(1u << i);
                         s[i / 4][i % 4] = -INFINITY;
                     }
@@ -461,12 +535,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attend(
             if (parts.scores && x < gn) {
                 float *at = parts.scores +
                             ((int64_t)b * q_heads + hq0 + x) * parts.score_stride + t0 + 4 * cg;
-                *(f32x4_t *)at = s[0];
-                *(f32x4_t *)(at + 16) = s[1];
+#pragma unroll
+                for (int u = 0; u < H; ++u) *(f32x4_t *)(at + 16 * u) = s[u];
             }
             float top = s[0][0];
 #pragma unroll
-            for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i / 4][i % 4]);
+            for (int i = 1; i < NP; ++i) top = fmaxf(top, s[i / 4][i % 4]);
             if (__any(top > m)) {
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
@@ -483,56 +557,59 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attend(
                     for (int i = 0; i < 4; ++i) acc[e][i] *= fr[i];
             }
             // nothing seen yet: every s is -infinity, and p is 0
-            const float ref = (m == -INFINITY ? 0.0f : m) - (DT == KV_F16 ? 15.0f : 0.0f);
-            float p[8];
+            const float ref = (m == -INFINITY ? 0.0f : m) - (PV == kTwoHalf ? 15.0f : 0.0f);
+            float p[NP];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < NP; ++i) {
                 p[i] = pow2(s[i / 4][i % 4] - ref);
                 l += p[i];
             }
             if constexpr (DT == KV_I8) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p[i] *= vsc[i / 4][i % 4];
+                for (int i = 0; i < NP; ++i) p[i] *= vsc[i / 4][i % 4];
                 if (!whole) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
+                    for (int i = 0; i < NP; ++i)
                         if (!(in >> i & 1u)) p[i] = 0.0f;
                 }
             } else if (!whole) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < NP; ++j)
 #pragma unroll
                     for (int k = 0; k < NC; ++k)
 #pragma unroll
                         for (int i = 0; i < VW; ++i)
                             if (!(in >> j & 1u)) vw[j][k][i] = 0;
             }
-            Split<DT> ps;
-            ps.set(p);
+            {
+                Split<PV> ps;
+                ps.set(p);
 #pragma unroll
-            for (int k = 0; k < NC; ++k)
+                for (int k = 0; k < NC; ++k)
 #pragma unroll
-                for (int e = 0; e < DC; ++e) {
-                    uint32_t v[8];
-                    if constexpr (DT == KV_F32) {
+                    for (int e = 0; e < DC; ++e) {
+                        uint32_t v[8];
+                        if constexpr (DT == KV_F32) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] = vw[j][k][e];
-                    } else if constexpr (DT == KV_I8) {
+                            for (int j = 0; j < 8; ++j) v[j] = vw[j][k][e];
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            v[j] = hi16_pair(fbits(code_at(vw[2 * j][k][e / 4], e % 4)),
-                                             fbits(code_at(vw[2 * j + 1][k][e / 4], e % 4)));
-                    } else {
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t *v0 = vw[2 * j][k], *v1 = vw[2 * j + 1][k];
+                                if constexpr (DT == KV_I8)
+                                    v[j] = hi16_pair(fbits(code_at(v0[e / 4], e % 4)),
+                                                     fbits(code_at(v1[e / 4], e % 4)));
+                                else
+                                    v[j] = e % 2 ? hi16_pair(v0[e / 2], v1[e / 2])
+                                                 : lo16_pair(v0[e / 2], v1[e / 2]);
+                            }
+                        }
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            v[j] = e % 2 ? hi16_pair(vw[2 * j][k][e / 2], vw[2 * j + 1][k][e / 2])
-                                         : lo16_pair(vw[2 * j][k][e / 2], vw[2 * j + 1][k][e / 2]);
+                        for (int r = Split<PV>::terms - 1; r >= 0; --r)
+                            acc[k * DC + e] = mfma8<PV>(ps.w[r], v, acc[k * DC + e]);
                     }
-#pragma unroll
-                    for (int r = P - 1; r >= 0; --r)
-                        acc[k * DC + e] = mfma8<DT>(ps.w[r], v, acc[k * DC + e]);
-                }
-            load_values(next);
+            }
+            load_values(next, more ? -1 : 0);
             pg = next;
         }
     }
@@ -542,10 +619,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attend(
     l += __shfl_xor(l, 32);
     if (cg == 0) s_m[wave][x] = m, s_l[wave][x] = l;
 #pragma unroll
-    for (int e = 0; e < NC * DC; ++e)
+    for (int k = 0; k < NC; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            s_acc[wave][4 * cg + i][DL * x + e] = acc[e][i];
+        for (int e = 0; e < DC; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s_acc[wave][4 * cg + i][(16 * k + x) * DC + e] = acc[k * DC + e][i];
     __syncthreads();
     const int64_t row = (int64_t)b * q_heads + hq0;
     const int64_t slot = (2 * (int64_t)blockIdx.x + (from == 0)) * 16;
@@ -606,7 +685,7 @@ __device__ __forceinline__ void joined(const float2 *stat, int w0, int count, in
     for (int o = 32; o > 0; o >>= 1) L += __shfl_xor(L, o);
 }
 
-constexpr int kWeighTile = 1024;
+constexpr int kWeighTile = 1024;  // four positions of each of 256 threads
 
 // Workgroups below `joins` join the parts of one (sequence, query head):
 // 1 << quad_bits threads take four dims each, the workgroup's 256 >> quad_bits
@@ -620,7 +699,7 @@ __global__ __launch_bounds__(256) void k_kv_join(const int32_t *__restrict__ tab
                                                  int64_t cols, int64_t joins, int64_t tiles,
                                                  int q_heads, int most, float unit, int quad_bits,
                                                  KvPool c) {
-    __shared__ float s_m[256], s_l[256];
+    __shared__ float s_m[16], s_l[16];
     __shared__ f32x4_t s_o[256];
     const int G = q_heads / c.heads, gblocks = (G + 15) / 16;
     if ((int64_t)blockIdx.x < joins) {
@@ -652,48 +731,72 @@ __global__ __launch_bounds__(256) void k_kv_join(const int32_t *__restrict__ tab
         }
         return;
     }
+    // a thread's four consecutive positions, all G heads
     const int64_t w = blockIdx.x - joins;
     const int64_t bh = w / tiles, b = bh / c.heads;
     const int h = (int)(bh % c.heads);
     const int n = kv_length(lens, b, most, nullptr);
-    const int lo = max((int)(w % tiles) * kWeighTile, starts ? max(starts[b], 0) : 0);
-    const int hi = min((int)(w % tiles + 1) * kWeighTile, n);
-    if (lo >= hi) return;
-    float p[kWeighTile / 256] = {};
-    for (int g0 = 0; g0 < G; g0 += 256) {
-        const int gn = min(256, G - g0);
+    const int lo = starts ? max(starts[b], 0) : 0;
+    const int t0 = (int)(w % tiles) * kWeighTile, t = t0 + 4 * (int)threadIdx.x;
+    if (t0 + kWeighTile <= lo || t0 >= n) return;
+    const bool mine = t + 4 > lo && t < n;
+    f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int g0 = 0; g0 < G; g0 += 16) {
+        const int gn = min(16, G - g0);
+        const int2 own = parts.owner[(b * c.heads + h) * gblocks + g0 / 16];
+        const int64_t row = b * q_heads + h * G + g0;
+        // 16 threads for each head: its maximum, and what its sum divides by
         __syncthreads();
-        for (int g = threadIdx.x >> 6; g < gn; g += 4) {
-            const int2 own = parts.owner[(b * c.heads + h) * gblocks + (g0 + g) / 16];
-            float M, L;
-            if (own.x == own.y) {
-                const float2 v = parts.whole[b * q_heads + h * G + g0 + g];
-                M = v.x, L = v.y;
+        {
+            const int g = threadIdx.x >> 4, i0 = threadIdx.x & 15;
+            const int count = own.y - own.x + 1;
+            float M = -INFINITY, L = 0.0f;
+            if (count == 1) {
+                if (g < gn && i0 == 0) {
+                    const float2 v = parts.whole[row + g];
+                    M = v.x, L = v.y;
+                }
             } else {
-                joined(parts.stat, own.x, own.y - own.x + 1, (g0 + g) % 16, M, L);
+                for (int i = i0; i < count; i += 16)
+                    M = fmaxf(M, parts.stat[part_slot(own.x, i) + g].x);
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
+                for (int i = i0; i < count; i += 16) {
+                    const float2 v = parts.stat[part_slot(own.x, i) + g];
+                    if (v.y != 0.0f) L += pow2(v.x - M) * v.y;
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) L += __shfl_xor(L, o);
             }
-            if ((threadIdx.x & 63) == 0) s_m[g] = M, s_l[g] = L == 0.0f ? 0.0f : unit / L;
+            if (i0 == 0) s_m[g] = M, s_l[g] = L == 0.0f ? 0.0f : unit / L;
         }
         __syncthreads();
-        for (int g = 0; g < gn; ++g) {
+        if (!mine) continue;
+        const float *from = parts.scores + row * parts.score_stride + t;
+        auto grow = [&](int g, const f32x4_t &s) {
             const float M = s_m[g], f = s_l[g];
-            const float *from =
-                parts.scores + (b * q_heads + h * G + g0 + g) * parts.score_stride;
 #pragma unroll
-            for (int i = 0; i < kWeighTile / 256; ++i) {
-                const int t = lo + (int)threadIdx.x + 256 * i;
-                if (t < hi && f != 0.0f) p[i] += pow2(from[t] - M) * f;
-            }
+            for (int i = 0; i < 4; ++i)
+                if (f != 0.0f) p[i] += pow2(s[i] - M) * f;
+        };
+        int g = 0;
+        for (; g + 4 <= gn; g += 4) {
+            f32x4_t s[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s[j] = *(const f32x4_t *)(from + (int64_t)(g + j) * parts.score_stride);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) grow(g + j, s[j]);
         }
+        for (; g < gn; ++g) grow(g, *(const f32x4_t *)(from + (int64_t)g * parts.score_stride));
     }
-    const int32_t *tab = table + b * cols;
+    if (!mine) return;
+    const int page = table[b * cols + (min(t, n - 1) >> c.shift)];
+    if (!kv_page_ok(c, page)) return;
+    const int64_t at = kv_row(c, page, h, t & ((1 << c.shift) - 1));
 #pragma unroll
-    for (int i = 0; i < kWeighTile / 256; ++i) {
-        const int t = lo + (int)threadIdx.x + 256 * i;
-        if (t >= hi) continue;
-        const int page = tab[t >> c.shift];
-        if (kv_page_ok(c, page)) c.weight[kv_row(c, page, h, t & ((1 << c.shift) - 1))] += p[i];
-    }
+    for (int i = 0; i < 4; ++i)
+        if (t + i >= lo && t + i < n) c.weight[at + i] += p[i];
 }
 
 }  // namespace
@@ -731,22 +834,23 @@ hipError_t launch_kv_attend(const KvPool &c, int dtype, const float *q, int64_t 
                            q_stride, cols, c, out, parts, d_status);
         return hipGetLastError();
     };
-#define KV_BY_DIM(DT)                                          \
-    (c.dim <= 64    ? go(k_kv_attend<DT, 2, 4>)                \
-     : c.dim <= 96  ? go(k_kv_attend<DT, 3, 8>)                \
-     : c.dim <= 128 ? go(k_kv_attend<DT, 4, 8>)                \
-                    : go(k_kv_attend<DT, 8, 16>))
-    hipError_t e = dtype == KV_F32    ? KV_BY_DIM(KV_F32)
-                   : dtype == KV_F16  ? KV_BY_DIM(KV_F16)
-                   : dtype == KV_BF16 ? KV_BY_DIM(KV_BF16)
-                                      : KV_BY_DIM(KV_I8);
+#define KV_BY_DIM(DT, PAIR)                                          \
+    (c.dim <= 64    ? go(k_kv_attend<DT, 2, 4, PAIR>)                \
+     : c.dim <= 96  ? go(k_kv_attend<DT, 3, 8, PAIR>)                \
+     : c.dim <= 128 ? go(k_kv_attend<DT, 4, 8, PAIR>)                \
+                    : go(k_kv_attend<DT, 8, 16, PAIR>))
+    hipError_t e = dtype == KV_F32    ? KV_BY_DIM(KV_F32, false)
+                   : dtype == KV_F16  ? KV_BY_DIM(KV_F16, false)
+                   : dtype == KV_BF16 ? KV_BY_DIM(KV_BF16, false)
+                   : c.dim < 16       ? go(k_kv_attend<KV_I8, 2, 4, false>)
+                                      : KV_BY_DIM(KV_I8, true);
 #undef KV_BY_DIM
     if (e != hipSuccess || second == 0) return e;
     int quad_bits = 1;
     while (4 << quad_bits < c.dim) ++quad_bits;
     hipLaunchKernelGGL(k_kv_join, dim3((unsigned)second), dim3(256), 0, stream, table, lens,
                        starts, out, parts, cols, joins, tiles, (int)q_heads, (int)max_len,
-                       dtype == KV_F16 ? 32768.0f : 1.0f, quad_bits, c);
+                       dtype == KV_F16 ? kHalfUnit : 1.0f, quad_bits, c);
     return hipGetLastError();
 }
 

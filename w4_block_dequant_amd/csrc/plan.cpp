@@ -472,7 +472,7 @@ KvAttendPlan plan_kv_attend(int64_t seqs, int64_t q_heads, int64_t heads, int64_
     p.groups = seqs * heads * cdiv(q_heads / heads, 16) * cdiv(max_len > 0 ? max_len : 1, 128);
     if (p.groups > fit) p.groups = fit;
     p.split = max_len > 128;
-    p.score_stride = (int64_t)align_up((size_t)max_len, 32);
+    p.score_stride = (int64_t)align_up((size_t)max_len, 64);  // whole tiles
     const size_t rows = (size_t)(seqs * q_heads);
     const size_t blocks = (size_t)(seqs * heads * cdiv(q_heads / heads, 16));
     size_t at = 0;
