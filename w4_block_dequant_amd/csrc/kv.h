@@ -80,4 +80,22 @@ __device__ __forceinline__ float order_value(uint32_t key) {
     return __builtin_bit_cast(float, key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
 
+// Sums over a wave in six additions: every lane's sum of itself and the lanes
+// below, and the whole wave's.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int scan_step(int v) {
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+    v = scan_step<0x111, 0xF>(v);  // from 1, 2, 4, 8 lanes below, within 16
+    v = scan_step<0x112, 0xF>(v);
+    v = scan_step<0x114, 0xF>(v);
+    v = scan_step<0x118, 0xF>(v);
+    v = scan_step<0x142, 0xA>(v);  // lanes 15 and 47 to the 16 above
+    return scan_step<0x143, 0xC>(v);  // lane 31 to the upper half
+}
+__device__ __forceinline__ int wave_sum(int v) {
+    return __builtin_amdgcn_readlane(wave_scan(v), 63);
+}
+
 }  // namespace w4

@@ -8,20 +8,22 @@
 //
 // Selection.  A weight's key is its value in an order that unsigned integers
 // have.  The keys are kept in registers (up to 32 in a lane; sequences past
-// 32768 are read again) and narrowed down by histograms of 256 bins: first over the
-// range from the smallest to the largest key, then over the bin in which the
-// wanted count is reached, until that bin is wanted whole or is one key.  Of a
-// few thousand keys with distinct weights that takes two or three histograms;
-// equal ones at most four.  Rows that tie with the last one stay in order of
-// position: wave w owns the w-th stretch of positions, so counts of the waves
-// before it place its rows.
+// 32768 are read again) and narrowed down by histograms of 2048 bins: first over
+// the range from the smallest to the largest key, then over the bin in which the
+// wanted count is reached, until that bin is wanted whole or is one key.  Of
+// distinct weights that takes two histograms; equal ones at most three.  Rows
+// that tie with the last one stay in order of position: wave w owns the w-th
+// stretch of positions, so counts of the waves before it place its rows.
 #include "kv.h"
 #include "launch.h"
 
 namespace w4 {
 namespace {
 
-constexpr int kSelWaves = 16;
+constexpr int kSelWaves = 16, kSelThreads = 64 * kSelWaves;
+constexpr int kBins = 2048;   // two to a thread
+constexpr int kBinBits = 11;
+constexpr int kBatch = 16;    // weights of a lane on their way at once
 
 __device__ __forceinline__ uint32_t evict_key(float w) {
     return __builtin_isnan(w) ? 0u : order_key(w);
@@ -29,11 +31,11 @@ __device__ __forceinline__ uint32_t evict_key(float w) {
 
 // R: keys of a lane held in registers (0: read again each time).
 template <int R>
-__global__ __launch_bounds__(64 * kSelWaves) void k_kv_select(
+__global__ __launch_bounds__(kSelThreads) void k_kv_select(
     const int32_t *__restrict__ table, const int32_t *__restrict__ lens, int64_t cols, int most,
     int keep, int recent, KvPool c, int32_t *kept, int32_t *lens_out, int *d_status) {
-    __shared__ uint32_t s_hist[256];
-    __shared__ uint32_t s_low[kSelWaves], s_high[kSelWaves], s_pick[4];
+    __shared__ uint32_t s_hist[kBins];
+    __shared__ uint32_t s_low[kSelWaves], s_high[kSelWaves], s_pick[3];
     const int64_t b = blockIdx.x / c.heads;
     const int h = (int)(blockIdx.x % c.heads);
     const int lane = threadIdx.x & 63;
@@ -42,43 +44,57 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_kv_select(
     const int n = min(L, keep);
     int32_t *to = kept + (int64_t)blockIdx.x * keep;
     if (h == 0 && threadIdx.x == 0) lens_out[b] = n;
-    for (int i = n + (int)threadIdx.x; i < keep; i += 64 * kSelWaves) to[i] = -1;
+    for (int i = n + (int)threadIdx.x; i < keep; i += kSelThreads) to[i] = -1;
     if (L <= keep) {
-        for (int i = threadIdx.x; i < n; i += 64 * kSelWaves) to[i] = i;
+        for (int i = threadIdx.x; i < n; i += kSelThreads) to[i] = i;
         return;
     }
     // of the first m positions `want` stay; the newest r all do
     const int r = min(recent, keep), want = keep - r, m = L - r;
-    for (int i = threadIdx.x; i < r; i += 64 * kSelWaves) to[want + i] = m + i;
+    for (int i = threadIdx.x; i < r; i += kSelThreads) to[want + i] = m + i;
     if (want == 0) return;
 
     const int32_t *tab = table + b * cols;
-    const int rounds = (m + 64 * kSelWaves - 1) / (64 * kSelWaves);  // at most R, if R > 0
+    const int rounds = (m + kSelThreads - 1) / kSelThreads;  // at most R, if R > 0
     const int first = wave * rounds * 64 + lane;
-    auto read = [&](int t) {
-        const int page = tab[t >> c.shift];
-        return kv_page_ok(c, page)
-                   ? evict_key(c.weight[kv_row(c, page, h, t & ((1 << c.shift) - 1))])
-                   : 0u;
+    constexpr int B = R > 0 && R < kBatch ? R : kBatch;
+    // keys of rounds i0 .. i0 + B: all their pages, then all their weights; places
+    // past m read position m - 1's, a foreign page counts as weight lowest
+    auto read = [&](uint32_t *out, int i0) {
+        int page[B];
+        float w[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) page[i] = tab[min(first + 64 * (i0 + i), m - 1) >> c.shift];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int t = min(first + 64 * (i0 + i), m - 1);
+            w[i] = c.weight[kv_row(c, kv_page_ok(c, page[i]) ? page[i] : 0, h,
+                                   t & ((1 << c.shift) - 1))];
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i) out[i] = kv_page_ok(c, page[i]) ? evict_key(w[i]) : 0u;
     };
-    uint32_t held[R ? R : 1];
+    uint32_t held[R > 0 ? R / B : 1][B];
     if constexpr (R > 0) {
 #pragma unroll
-        for (int i = 0; i < R; ++i)
-            held[i] = i < rounds && first + 64 * i < m ? read(first + 64 * i) : 0u;
+        for (int i = 0; i < R / B; ++i)
+            if (i * B < rounds) read(held[i], i * B);
     }
-    // f(key, position) for every position of the lane
+    // f(key, position, whether it is one of the m) for every place of the lane
     auto each = [&](auto f) {
         if constexpr (R > 0) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 if (i >= rounds) break;
-                f(held[i], first + 64 * i, first + 64 * i < m);
+                f(held[i / B][i % B], first + 64 * i, first + 64 * i < m);
             }
         } else {
-            for (int i = 0; i < rounds; ++i) {
-                const int t = first + 64 * i;
-                f(t < m ? read(t) : 0u, t, t < m);
+            for (int i0 = 0; i0 < rounds; i0 += B) {
+                read(held[0], i0);
+#pragma unroll
+                for (int i = 0; i < B; ++i)
+                    if (i0 + i < rounds)
+                        f(held[0][i], first + 64 * (i0 + i), first + 64 * (i0 + i) < m);
             }
         }
     };
@@ -94,44 +110,36 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_kv_select(
         high = max(high, (uint32_t)__shfl_xor((int)high, o));
     }
     if (lane == 0) s_low[wave] = low, s_high[wave] = high;
+    s_hist[threadIdx.x] = 0;
+    s_hist[threadIdx.x + kSelThreads] = 0;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kSelWaves; ++w) low = min(low, s_low[w]), high = max(high, s_high[w]);
 
     // keys [low, low + span] hold the last row that stays; `left` of them stay
     uint32_t span = high - low, left = (uint32_t)want;
-    int shift = max(0, 24 - __builtin_clz(span | 1u));
+    int shift = max(0, 32 - kBinBits - __builtin_clz(span | 1u));
     uint32_t least, ties;  // rows above `least` stay, and the first `ties` rows equal to it
     for (;;) {
-        if (threadIdx.x < 256) s_hist[threadIdx.x] = 0;
-        __syncthreads();
         each([&](uint32_t key, int, bool in) {
             if (in && key >= low && key - low <= span) atomicAdd(&s_hist[(key - low) >> shift], 1u);
         });
         __syncthreads();
-        if (wave == 0) {
-            // lane: bins 255 - 4 lane .. 252 - 4 lane, counted from the top
-            uint32_t n4[4], sum = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) n4[i] = s_hist[255 - 4 * lane - i], sum += n4[i];
-            uint32_t upto = sum;
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const uint32_t v = (uint32_t)__shfl_up((int)upto, o);
-                if (lane >= o) upto += v;
-            }
-            uint32_t above = upto - sum;
-            if (above < left && upto >= left) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (above < left && above + n4[i] >= left) {
-                        s_pick[0] = 255 - 4 * lane - i;
-                        s_pick[1] = above;
-                        s_pick[2] = n4[i];
-                    }
-                    above += n4[i];
-                }
-            }
+        // a thread's two bins, counted from the top, and what lies above them
+        const int top = kBins - 1 - 2 * (int)threadIdx.x;
+        const uint32_t n0 = s_hist[top], n1 = s_hist[top - 1];
+        const uint32_t upto = (uint32_t)wave_scan((int)(n0 + n1));
+        if (lane == 63) s_low[wave] = upto;
+        s_hist[top] = 0;  // for the next histogram
+        s_hist[top - 1] = 0;
+        __syncthreads();
+        uint32_t above = upto - n0 - n1;
+        for (int w = 0; w < wave; ++w) above += s_low[w];
+        if (above < left && above + n0 + n1 >= left) {
+            const bool second = above + n0 < left;
+            s_pick[0] = (uint32_t)(second ? top - 1 : top);
+            s_pick[1] = second ? above + n0 : above;
+            s_pick[2] = second ? n1 : n0;
         }
         __syncthreads();
         low += s_pick[0] << shift;
@@ -147,25 +155,27 @@ __global__ __launch_bounds__(64 * kSelWaves) void k_kv_select(
             break;
         }
         span = (1u << shift) - 1;
-        shift = max(0, shift - 8);
+        shift = max(0, shift - kBinBits);
     }
 
-    uint32_t over = 0, same = 0;
+    int over = 0, same = 0;
     each([&](uint32_t key, int, bool in) {
-        over += (uint32_t)__popcll(__ballot(in && key > least));
-        same += (uint32_t)__popcll(__ballot(in && key == least));
+        over += in && key > least;
+        same += in && key == least;
     });
-    __syncthreads();
-    if (lane == 0) s_low[wave] = over, s_high[wave] = same;
+    over = wave_sum(over), same = wave_sum(same);
+    if (lane == 0) s_high[wave] = (uint32_t)over, s_hist[wave] = (uint32_t)same;
     __syncthreads();
     uint32_t base = 0, tied = 0;  // rows of the waves before: above, and equal
-    for (int w = 0; w < wave; ++w) base += s_low[w], tied += s_high[w];
-    const uint64_t below = (1ull << lane) - 1;
+    for (int w = 0; w < wave; ++w) base += s_high[w], tied += s_hist[w];
+    auto below = [](uint64_t mask, uint32_t from) {  // bits of the lanes below, plus from
+        return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                         __builtin_amdgcn_mbcnt_lo((uint32_t)mask, from));
+    };
     each([&](uint32_t key, int t, bool in) {
         const uint64_t up = __ballot(in && key > least), eq = __ballot(in && key == least);
-        const uint32_t rank = tied + (uint32_t)__popcll(eq & below);  // among the equal ones
-        const uint32_t place =
-            base + (uint32_t)__popcll(up & below) + min(rank, ties);
+        const uint32_t rank = below(eq, tied);  // among the equal ones
+        const uint32_t place = below(up, base) + min(rank, ties);
         if (in && (key > least || (key == least && rank < ties))) to[place] = t;
         base += (uint32_t)__popcll(up);
         tied += (uint32_t)__popcll(eq);
@@ -244,12 +254,12 @@ hipError_t launch_kv_evict(const KvPool &c, int row_bytes, const int32_t *table,
                            int32_t *kept, int32_t *lens_out, int *d_status, hipStream_t stream) {
     const int64_t bh = seqs * c.heads;
     auto select = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)bh), dim3(64 * kSelWaves), 0, stream, table,
+        hipLaunchKernelGGL(kernel, dim3((unsigned)bh), dim3(kSelThreads), 0, stream, table,
                            lens, cols, (int)max_len, (int)keep, (int)recent, c, kept, lens_out,
                            d_status);
         return hipGetLastError();
     };
-    const int64_t rounds = (max_len + 64 * kSelWaves - 1) / (64 * kSelWaves);
+    const int64_t rounds = (max_len + kSelThreads - 1) / kSelThreads;
     hipError_t e = rounds <= 4    ? select(k_kv_select<4>)
                    : rounds <= 16 ? select(k_kv_select<16>)
                    : rounds <= 32 ? select(k_kv_select<32>)
