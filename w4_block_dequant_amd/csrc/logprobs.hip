@@ -17,9 +17,12 @@
 // threshold, a key that at least `top` keys of the row reach: at first the
 // top-th largest of the wave's lane maxima, later the top-th key of the list
 // or, if that is larger, any other wave's.  Keys past the threshold enter the
-// queue; at 64 they are sorted and merged into the list (of 50,000 logits drawn
-// alike some hundred ever enter a queue).  Which keys get so far depends on
-// the waves' timing, the `top` largest do not.
+// queue; at 64 they are sorted and merged into the list.  Of logits drawn alike
+// few ever do: if no queue filled up, the keys of all queues that pass the last
+// threshold are sorted at once where they are at most 64; otherwise the waves'
+// lists are merged two by two.  Which keys get so far depends on the waves'
+// timing, the `top` largest do not.  For the largest entry alone a
+// lane keeps its own best key and the keys are compared at the end.
 //
 // Sorting exchanges lanes by DPP and permlane swaps: compare-and-exchange with
 // lane ^ (2^i - 1), then lane ^ 2^j downwards, so that every step keeps the
@@ -177,8 +180,24 @@ struct LpOut {
     int *d_status;
 };
 
+// The given token's logit, read before it is needed.
+struct LpToken {
+    bool in = false;
+    float x = 0.0f;
+};
+__device__ __forceinline__ LpToken lp_token(const LpOut &o, int64_t row, const float *x,
+                                            int64_t N) {
+    LpToken t;
+    if (o.logprob) {
+        const int64_t token = o.tokens[row];
+        t.in = token >= 0 && token < N;
+        if (t.in) t.x = x[token];
+    }
+    return t;
+}
+
 // What a row's maximum, sums and list come to; wave 0 of a workgroup.
-__device__ __forceinline__ void lp_finish(const LpOut &o, int64_t row, const float *x, int64_t N,
+__device__ __forceinline__ void lp_finish(const LpOut &o, int64_t row, const LpToken &token,
                                           int top, const LpSums &r, uint64_t list) {
     const int lane = threadIdx.x;
     const bool bad = __builtin_isnan(r.S), none = r.m == -INFINITY && !bad;
@@ -189,10 +208,8 @@ __device__ __forceinline__ void lp_finish(const LpOut &o, int64_t row, const flo
     if (lane == 0) {
         if (bad) set_status(o.d_status, W4_ERR_NONFINITE);
         if (o.logprob) {
-            const int64_t token = o.tokens[row];
-            const bool in = token >= 0 && token < N;
-            if (!in) set_status(o.d_status, W4_ERR_BAD_SHAPE);
-            o.logprob[row] = in ? log_p(x[token]) : NAN;
+            if (!token.in) set_status(o.d_status, W4_ERR_BAD_SHAPE);
+            o.logprob[row] = token.in ? log_p(token.x) : NAN;
         }
         if (o.entropy) o.entropy[row] = bad ? NAN : none ? 0.0f : logS - r.W / r.S;
     }
@@ -202,14 +219,31 @@ __device__ __forceinline__ void lp_finish(const LpOut &o, int64_t row, const flo
     }
 }
 
+// What is kept of the largest entries.
+enum LpMode { kNone, kOne, kList };
+
+__device__ __forceinline__ uint64_t key_of(float v, uint32_t n) {
+    return (uint64_t)order_key(v) << 32 | (uint32_t)~n;
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+    v = max(v, lane_xor<1>(v));
+    v = max(v, lane_xor<2>(v));
+    v = max(v, lane_xor<4>(v));
+    v = max(v, lane_xor<8>(v));
+    v = max(v, lane_xor<16>(v));
+    return max(v, lane_xor<32>(v));
+}
+
 // Grid: rows x chunks.  chunks == 1: straight to the outputs; else (m, S, W)
 // and the `top` largest keys of each chunk to the workspace.
+template <LpMode MODE>
 __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restrict__ logits,
                                                             int64_t N, int64_t ld, int top,
                                                             int chunks, int chunk, LpOut o,
                                                             float4 *sums, uint64_t *keys) {
     __shared__ uint64_t s_key[kLpWaves][128];  // queues, later lists
-    __shared__ uint64_t s_limit;
+    __shared__ uint64_t s_limit, s_last[64];
+    __shared__ int s_flushed, s_count;
     __shared__ LpSums s_sum[kLpWaves];
     const int64_t row = blockIdx.x / chunks;
     const int piece = (int)(blockIdx.x % chunks);
@@ -219,8 +253,12 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restr
     // 32 bits unsigned: N is below 2^31 and a wave looks at most 2^14 ahead of it
     const uint32_t begin = (uint32_t)piece * (uint32_t)chunk;
     const uint32_t end = min(begin + (uint32_t)chunk, (uint32_t)N);
-    if (threadIdx.x == 0) s_limit = 0;
-    __syncthreads();
+    LpToken token;
+    if (chunks == 1 && wave == 0) token = lp_token(o, row, x, N);
+    if (MODE == kList) {
+        if (threadIdx.x == 0) s_limit = 0, s_flushed = 0, s_count = 0;
+        __syncthreads();
+    }
 
     LpSums r = {-INFINITY, 0.0f, 0.0f};
     uint64_t list = 0, limit = 0;  // descending keys; the threshold (0: none yet)
@@ -290,7 +328,19 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restr
             r.S += e;
             r.W = fmaf(e, fmaxf(d, -1e30f), r.W);
         }
-        if (top > 0) {
+        if constexpr (MODE == kOne) {
+            // equal values keep the lower index, which came first
+            if (fresh || best > reach) {
+                reach = best;
+                uint32_t j = 0;
+#pragma unroll
+                for (int i = 4 * kLpLoads - 1; i >= 0; --i)
+                    if (v[i / 4][i % 4] == best) j = 256 * (i / 4) + i % 4;
+                list = key_of(best, at + 4 * lane + j);
+            }
+            fresh = false;
+        }
+        if constexpr (MODE == kList) {
             if (fresh) {
                 uint32_t first = order_key(best);
                 sort64(first);
@@ -313,7 +363,7 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restr
                     for (int i = 1; i < 4 * kLpLoads; ++i)
                         if (i == j) w = v[i / 4][i % 4];
                     const uint32_t n = at + 256 * (j / 4) + 4 * lane + j % 4;
-                    const uint64_t key = (uint64_t)order_key(w) << 32 | (uint32_t)~n;
+                    const uint64_t key = key_of(w, n);
                     const bool in = bits != 0 && n < end && key > limit;
                     bits &= bits - 1;
                     const uint64_t mask = __ballot(in);
@@ -324,21 +374,49 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restr
                                                  __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] =
                             key;
                     queued += __popcll(mask);
-                    if (queued >= 64) flush();
+                    if (queued >= 64) {
+                        flush();
+                        if (lane == 0) s_flushed = 1;
+                    }
                 }
             }
         }
     }
-    if (top > 0 && queued > 0) flush();
     r = lp_wave(r);
     if (lane == 0) s_sum[wave] = r;
-    if (top > 0) {
-        // the waves' lists, two by two
+    if constexpr (MODE == kOne) {
+        list = wave_max(list);
+        if (lane == 0) s_key[wave][0] = list;
+    }
+    if constexpr (MODE == kList) {
+        __syncthreads();
+        const bool sparse = s_flushed == 0;
+        if (sparse) {
+            // without a flush the threshold is a value: all its keys are larger
+            const uint64_t k = lane < queued ? s_key[wave][lane] : 0;
+            const uint64_t mask = __ballot(k > s_limit);
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&s_count, (int)__popcll(mask));
+            at = __builtin_amdgcn_readfirstlane(at) +
+                 (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                                __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+            if (k > s_limit && at < 64) s_last[at] = k;
+        }
+        __syncthreads();
+        if (sparse && s_count <= 64) {
+            if (wave == 0) {
+                list = lane < s_count ? s_last[lane] : 0;
+                sort64(list);
+            }
+        } else {
+            if (queued > 0) flush();
+            __syncthreads();  // queues and lists share their memory
 #pragma unroll
-        for (int half = kLpWaves / 2; half > 0; half >>= 1) {
-            if (wave >= half && wave < 2 * half) s_key[wave][lane] = list;
-            __syncthreads();
-            if (wave < half) merge64(list, s_key[wave + half][63 - lane]);
+            for (int half = kLpWaves / 2; half > 0; half >>= 1) {
+                if (wave >= half && wave < 2 * half) s_key[wave][lane] = list;
+                __syncthreads();
+                if (wave < half) merge64(list, s_key[wave + half][63 - lane]);
+            }
         }
     } else {
         __syncthreads();
@@ -346,9 +424,12 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restr
     if (wave != 0) return;
     r = s_sum[0];
 #pragma unroll
-    for (int w = 1; w < kLpWaves; ++w) r = lp_join(r, s_sum[w]);
+    for (int w = 1; w < kLpWaves; ++w) {
+        r = lp_join(r, s_sum[w]);
+        if (MODE == kOne) list = max(list, s_key[w][0]);
+    }
     if (chunks == 1) {
-        lp_finish(o, row, x, N, top, r, list);
+        lp_finish(o, row, token, top, r, list);
     } else {
         if (lane == 0) sums[blockIdx.x] = make_float4(r.m, r.S, r.W, 0.0f);
         if (lane < top) keys[(int64_t)blockIdx.x * top + lane] = list;
@@ -357,6 +438,7 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restr
 
 // One workgroup joins the chunks of a row: its four waves take every fourth
 // chunk's list, which is in descending order already.
+template <LpMode MODE>
 __global__ __launch_bounds__(256) void k_logprobs_join(const float *__restrict__ logits, int64_t N,
                                                        int64_t ld, int top, int chunks, LpOut o,
                                                        const float4 *__restrict__ sums,
@@ -365,10 +447,29 @@ __global__ __launch_bounds__(256) void k_logprobs_join(const float *__restrict__
     const int64_t row = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     uint64_t list = 0;
-    if (top > 0) {
+    LpToken token;
+    LpSums r = {-INFINITY, 0.0f, 0.0f};
+    if (wave == 0) {
+        token = lp_token(o, row, logits + row * ld, N);
+        for (int i = lane; i < chunks; i += 64) {
+            const float4 v = sums[row * chunks + i];
+            r = lp_join(r, LpSums{v.x, v.y, v.z});
+        }
+    }
+    if constexpr (MODE == kOne) {
+        if (wave == 0) {
+            for (int i = lane; i < chunks; i += 64) list = max(list, keys[row * chunks + i]);
+            list = wave_max(list);
+        }
+    }
+    if constexpr (MODE == kList) {
+        auto load = [&](int i) {
+            return i < chunks && 63 - lane < top ? keys[(row * chunks + i) * top + 63 - lane] : 0;
+        };
+        uint64_t next = load(wave);
         for (int i = wave; i < chunks; i += 4) {
-            const uint64_t k =
-                63 - lane < top ? keys[(row * chunks + i) * top + 63 - lane] : 0;
+            const uint64_t k = next;
+            next = load(i + 4);
             merge64(list, k);
         }
 #pragma unroll
@@ -378,14 +479,7 @@ __global__ __launch_bounds__(256) void k_logprobs_join(const float *__restrict__
             if (wave < half) merge64(list, s_key[wave + half][63 - lane]);
         }
     }
-    if (wave != 0) return;
-    LpSums r = {-INFINITY, 0.0f, 0.0f};
-    for (int i = lane; i < chunks; i += 64) {
-        const float4 v = sums[row * chunks + i];
-        r = lp_join(r, LpSums{v.x, v.y, v.z});
-    }
-    r = lp_wave(r);
-    lp_finish(o, row, logits + row * ld, N, top, r, list);
+    if (wave == 0) lp_finish(o, row, token, top, lp_wave(r), list);
 }
 
 }  // namespace
@@ -403,13 +497,18 @@ hipError_t launch_logprobs(const float *logits, int64_t M, int64_t N, int64_t ld
     const LpOut o = {tokens, logprob, entropy, top_logprob, top_ids, d_status};
     float4 *sums = p.chunks > 1 ? (float4 *)workspace : nullptr;
     uint64_t *keys = p.chunks > 1 ? (uint64_t *)((char *)workspace + p.keys) : nullptr;
-    hipLaunchKernelGGL(k_logprobs, dim3((unsigned)(M * p.chunks)), dim3(64 * kLpWaves), 0, stream,
-                       logits, N, ld, (int)top, (int)p.chunks, (int)p.chunk, o, sums, keys);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.chunks == 1) return e;
-    hipLaunchKernelGGL(k_logprobs_join, dim3((unsigned)M), dim3(256), 0, stream, logits, N, ld,
-                       (int)top, (int)p.chunks, o, sums, keys);
-    return hipGetLastError();
+    auto go = [&](auto kernel, auto join) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(M * p.chunks)), dim3(64 * kLpWaves), 0, stream,
+                           logits, N, ld, (int)top, (int)p.chunks, (int)p.chunk, o, sums, keys);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess || p.chunks == 1) return e;
+        hipLaunchKernelGGL(join, dim3((unsigned)M), dim3(256), 0, stream, logits, N, ld, (int)top,
+                           (int)p.chunks, o, sums, keys);
+        return hipGetLastError();
+    };
+    return top == 0   ? go(k_logprobs<kNone>, k_logprobs_join<kNone>)
+           : top == 1 ? go(k_logprobs<kOne>, k_logprobs_join<kOne>)
+                      : go(k_logprobs<kList>, k_logprobs_join<kList>);
 }
 
 }  // namespace w4

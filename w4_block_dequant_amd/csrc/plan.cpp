@@ -494,10 +494,13 @@ LogprobsPlan plan_logprobs(int64_t M, int64_t N, int64_t top) {
     LogprobsPlan p;
     p.chunk = N;
     if (M <= 0) return p;
-    // two workgroups for each compute unit, none with less than 2048 logits
-    constexpr int64_t kWgs = 512, kLeast = 2048;
+    // two workgroups for each compute unit, none with less than 2048 logits, or
+    // 4096 if it has a list to sort (one row of 50257, top 5: 12.6 against 11.7 us;
+    // top 1 the other way, 7.7 against 8.0)
+    constexpr int64_t kWgs = 512;
+    const int64_t least = top > 1 ? 4096 : 2048;
     int64_t chunks = kWgs / M;
-    if (chunks > N / kLeast) chunks = N / kLeast;
+    if (chunks > N / least) chunks = N / least;
     if (chunks <= 1) return p;
     p.chunk = (int64_t)align_up((size_t)cdiv(N, chunks), 256);
     p.chunks = cdiv(N, p.chunk);
