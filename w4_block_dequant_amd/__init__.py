@@ -788,27 +788,30 @@ def lp_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: i
     if logits.dim() != 2:
         raise ValueError("logits must be [M, N]")
     M, N = logits.shape
-    if N > 1 and logits.stride(1) != 1:
+    ld, step = logits.stride()
+    if N > 1 and step != 1:
         raise ValueError("a row of logits must be contiguous")
-    ld = logits.stride(0) if M > 1 else N
-    dev = logits.device
+    if M <= 1:
+        ld = N
     logprob = None
     if tokens is not None:
         _dev(tokens, torch.int64, "tokens")
         if tokens.shape != (M,):
             raise ValueError("tokens must be [M]")
-        logprob = torch.empty(M, dtype=torch.float32, device=dev)
+        logprob = logits.new_empty(M)
     if d_status is not None:
         _dev(d_status, torch.int32, "d_status")
-    entropy = torch.empty(M, dtype=torch.float32, device=dev)
-    top_ids = torch.empty((M, max(top, 0)), dtype=torch.int64, device=dev)
-    top_logprob = torch.empty((M, max(top, 0)), dtype=torch.float32, device=dev)
+    entropy = logits.new_empty(M)
+    top_logprob = logits.new_empty((M, max(top, 0)))
+    top_ids = torch.empty((M, max(top, 0)), dtype=torch.int64, device=logits.device)
     if workspace is None:
-        ws, wsb = _workspace.get(dev, _lib.lp_logprobs_workspace_bytes(M, N, top))
+        need = _lib.lp_logprobs_workspace_bytes(M, N, top)
+        ws, wsb = _workspace.get(logits.device, need) if need else (None, 0)
     else:
         _dev(workspace, torch.uint8, "workspace")
         ws, wsb = workspace, workspace.numel()
     _check("lp_logprobs", _lib.lp_logprobs(
-        _ptr(logits), M, N, ld, _ptr(tokens), top, _ptr(logprob), _ptr(entropy), _ptr(top_ids),
-        _ptr(top_logprob), _ptr(ws), wsb, _ptr(d_status), _stream(dev)))
+        logits.data_ptr(), M, N, ld, _ptr(tokens), top, _ptr(logprob), entropy.data_ptr(),
+        top_ids.data_ptr(), top_logprob.data_ptr(), _ptr(ws), wsb, _ptr(d_status),
+        _stream(logits.device)))
     return logprob, entropy, top_ids, top_logprob

@@ -494,13 +494,17 @@ LogprobsPlan plan_logprobs(int64_t M, int64_t N, int64_t top) {
     LogprobsPlan p;
     p.chunk = N;
     if (M <= 0) return p;
-    // two workgroups for each compute unit, none with less than 2048 logits, or
-    // 4096 if it has a list to sort (one row of 50257, top 5: 12.6 against 11.7 us;
-    // top 1 the other way, 7.7 against 8.0)
+    // Two workgroups for each compute unit, none with less than 16384 logits, or
+    // 4096 if it has a list to sort (one row of 50257, top 5, pieces of 2048:
+    // 12.6 us, of 4096: 11.7).  One workgroup streams 65536 logits in less time
+    // than a second launch adds, without a list (one row of 50257, top 1: 8.3 us,
+    // in pieces and joined 7.7 but a launch of the host more; 58 rows 9.6 against
+    // 11.0; one row of 100003 12.6 against 10.1).
     constexpr int64_t kWgs = 512;
-    const int64_t least = top > 1 ? 4096 : 2048;
+    const int64_t least = top > 1 ? 4096 : 16384;
     int64_t chunks = kWgs / M;
     if (chunks > N / least) chunks = N / least;
+    if (top <= 1 && N <= 65536) chunks = 1;
     if (chunks <= 1) return p;
     p.chunk = (int64_t)align_up((size_t)cdiv(N, chunks), 256);
     p.chunks = cdiv(N, p.chunk);
