@@ -432,9 +432,13 @@ int kv_append(const kv_cache *cache, const float *k, int64_t k_stride, const flo
  * weight grows by the sum of p[h, t] over the G query heads of its key head; a
  * page whose weights grow must then belong to one sequence only.
  * fp32 arithmetic on the values that the cache's type holds, softmax
- * statistics and sums in fp32; deterministic.  Attended values must be finite:
+ * statistics and sums in fp32; deterministic.  (An fp16 cache: q and p enter as
+ * two fp16 terms each, exact to 2^-24 of themselves or 2^-40 of their row's
+ * largest, whichever is more.)  Attended values must be finite:
  * others make their head's outputs NaN or infinite.  max_len bounds lens for the
- * launch (0: cols * page_size); lens may be smaller by any amount.  The
+ * launch (0: cols * page_size); lens may be smaller by any amount.  The work is
+ * counted in int32: seqs * heads * ceil(G / 16) * (ceil(max_len / 128) + 2) must be
+ * below 2^31 (W4_ERR_BAD_SHAPE otherwise).  The
  * workspace (kv_attend_workspace_bytes, 256-byte aligned, any contents, not
  * shared with a call in flight on another stream) holds the parts that the
  * length is split into.                                                    */
@@ -461,8 +465,8 @@ int kv_attend(const kv_cache *cache, const float *q, int64_t q_stride, int64_t q
  * (int32 [seqs, cols_out], cols_out * page_size >= min(keep, max_len)), which must be
  * none of the pages read: the old pages, which other sequences may share, are
  * left as they are.  kept int32 [seqs, heads, keep]: the old positions, ascending,
- * then -1; lens_out int32 [seqs] = min(L, keep).  keep >= 1, recent >= 0.
- * max_len as in kv_attend; lengths below 2^24.  No workspace.               */
+ * then -1; lens_out int32 [seqs] = min(L, keep).  1 <= keep <= 2^24, recent >= 0,
+ * seqs * heads <= 65535.  max_len as in kv_attend, at most 2^24.  No workspace. */
 int kv_evict(const kv_cache *cache, const int32_t *table, int64_t seqs, int64_t cols,
              const int32_t *lens, int64_t max_len, int64_t keep, int64_t recent,
              const int32_t *table_out, int64_t cols_out, int32_t *kept, int32_t *lens_out,

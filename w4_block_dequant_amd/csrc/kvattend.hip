@@ -24,17 +24,26 @@
 // kernel joins them in order.  So results are deterministic.  No LDS and no
 // barrier in the loop over positions.
 //
+// Where the blocks are few, so that a workgroup has only some steps, crossing
+// from one block to the next would cost it as much as the steps: then the units
+// are parts of a block, of at least kPart steps, one to a workgroup.
+//
 // Tile.  Lane (c, x) = (lane / 16, lane % 16).
 //   Scores: the keys are the MFMA's A operand (row x = position t0 + 16 u + x,
-//   dims 32 b + 8 c .. + 7 of block b, u = 0, 1), the queries its B operand
-//   (column x = head x); the result leaves lane (c, x) with positions
-//   t0 + 16 u + 4 c + i (i = 0..3) of head x.
+//   u = 0, 1; eight of the 32 dims of a block, which eight is the lane's choice as
+//   long as the queries' agree), the queries its B operand (column x = head x);
+//   the result leaves lane (c, x) with positions t0 + 16 u + 4 c + i (i = 0..3)
+//   of head x.
 //   Output: those eight p are, in place, the A operand (row x = head x) of the
 //   product with the values if its k index 8 c + j stands for position
 //   4 c + j (j < 4) or 16 + 4 c + j - 4: nothing moves between lanes.  The lane
-//   reads the DL dims DL x .. of those eight positions' values, and the B
-//   operand of dim e is the e-th element of each (a 16-bit transpose within the
-//   lane, one v_perm for two elements); acc[e] leaves head 4 c + i, dim DL x + e.
+//   reads DL dims of those eight positions' values, and the B operand of its
+//   e-th dim is the e-th element of each (a 16-bit transpose within the lane, one
+//   v_perm for two elements); acc[e][i] is that dim of head 4 c + i.
+//   Which dims a lane takes is set so that each load instruction of 16 bytes a
+//   lane covers whole 64-byte lines of a row (fp32 in two halves of 16 dims, int8
+//   keys 16 codes to a lane): a line that two instructions touch is asked for
+//   twice.  16 x 4096 positions of 32 x 128: int8 127 -> 92 us, fp32 369 -> 316.
 //
 // Operands are exact or as good as fp32, sums are fp32 (the matrix cores'):
 //   bf16 cache: q and p are split exactly into three bf16 terms.
@@ -48,6 +57,14 @@
 // range get s = -infinity by selection and values of zero, whatever their
 // slots hold; an address is never formed from a table entry that the range
 // does not need or whose page the pool does not have.
+//
+// Measured (back to back, joining included; bytes: the attended keys and values):
+// 4 x 131072 positions of 8 x 128 bf16, 4 queries to a key head: 319 us, 6.7 TB/s;
+// 16 x 4096 of 32 heads: bf16 of 128 163 us, 6.6 TB/s; fp32 of 128 317 us, 6.8; int8 of
+// 128 92 us, 6.0, of 96 79 us, 5.3 (96-byte rows straddle lines); ragged batches of
+// 180-210 MB 3.5-4.1 TB/s (5 us of start, 4 of joining); one sequence of 4095 of
+// 32 x 96 bf16 17.2 us, 2.9 TB/s; 59 positions of 12 x 64 fp32 6.6 us, one launch
+// and a chain of loads (length, page, key).
 #include <math.h>
 
 #include "kv.h"
@@ -341,307 +358,309 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attend(
 
     int n = kv_length(lens, b, most, d_status), lo = first_of(b), steps = kv_steps(lo, n);
     for (int u = u0; u < u1;) {
-    // block vb of sequence b, its steps [from, to)
-    const int units = kv_units(steps, part);
-    const int vb = (u - base) / units, start = base + vb * units;
-    const int stop = min(u1, start + units);
-    const int even = part ? (steps + units - 1) / units : 0;
-    const int from = part ? (u - start) * even : max(u - start - kOpen, 0);
-    const int to = part ? min((u - start + 1) * even, steps) : stop - start - kOpen;
-    const int h = vb / gblocks, g0 = vb % gblocks * 16, gn = min(16, G - g0);
-    const int hq0 = h * G + g0;
-    const int first = kv_begin(lo) + from * kStep;
-    const int last = min(kv_begin(lo) + to * kStep, n);
-    const int32_t *tab = table + (int64_t)b * cols;
-    const bool whole_block = from == 0 && to == steps;
-    if (parts.owner && u == start && threadIdx.x == 0) {
-        // the workgroup of unit v is ((v + 1) groups - 1) / total
-        const int lead = part ? 0 : kOpen;
-        const int at = (int)(((uint64_t)(start + lead + 1) * groups - 1) / total);
-        const int end = (int)(((uint64_t)(start + units) * groups - 1) / total);
-        parts.owner[(int64_t)b * blocks + vb] = steps ? make_int2(at, end) : make_int2(0, 0);
-    }
-    if (to > from) {
-
-    auto find = [&](int t0) {
-        TilePages<H> p;
-#pragma unroll
-        for (int u = 0; u < H; ++u) {
-            // groups past the end read its page, and no entry past it
-            const int t = t0 + 16 * u;
-            const int page = tab[min(t, last - 1) >> c.shift];
-            p.ok[u] = kv_page_ok(c, page);
-            if (!p.ok[u]) set_status(d_status, W4_ERR_BAD_SHAPE);
-            p.row[u] = kv_row(c, p.ok[u] ? page : 0, h, t & mask);
+        // block vb of sequence b, its steps [from, to)
+        const int units = kv_units(steps, part);
+        const int vb = (u - base) / units, start = base + vb * units;
+        const int stop = min(u1, start + units);
+        const int even = part ? (steps + units - 1) / units : 0;
+        const int from = part ? (u - start) * even : max(u - start - kOpen, 0);
+        const int to = part ? min((u - start + 1) * even, steps) : stop - start - kOpen;
+        const int h = vb / gblocks, g0 = vb % gblocks * 16, gn = min(16, G - g0);
+        const int hq0 = h * G + g0;
+        const int first = kv_begin(lo) + from * kStep;
+        const int last = min(kv_begin(lo) + to * kStep, n);
+        const int32_t *tab = table + (int64_t)b * cols;
+        const bool whole_block = from == 0 && to == steps;
+        if (parts.owner && u == start && threadIdx.x == 0) {
+            // the workgroup of unit v is ((v + 1) groups - 1) / total
+            const int lead = part ? 0 : kOpen;
+            const int at = (int)(((uint64_t)(start + lead + 1) * groups - 1) / total);
+            const int end = (int)(((uint64_t)(start + units) * groups - 1) / total);
+            parts.owner[(int64_t)b * blocks + vb] = steps ? make_int2(at, end) : make_int2(0, 0);
         }
-        return p;
-    };
+        if (to > from) {
 
-    // `live` 0: every lane reads the group's first bytes (a load that nothing
-    // uses costs a cache line then, and no branch)
-    uint32_t kw[H][NB][KW];
-    uint32_t vw[NP][NC][VW];
-    f32x4_t ksc[H], vsc[H];
-    auto load_keys = [&](const TilePages<H> &p, int live) {
-#pragma unroll
-        for (int u = 0; u < H; ++u) {
-            const char *base = (const char *)c.k + p.row[u] * row_bytes;
-#pragma unroll
-            for (int k = 0; k < NB; ++k) {
-                if (k >= 2 * PAIRS) {
-#pragma unroll
-                    for (int i = 0; i < KL; ++i)
-                        load_words<8 * ES / KL, NT>(base + (koff[k * KL + i] & live),
-                                                kw[u][k] + i * KW / KL);
-                } else if (k % 2 == 0) {
-                    uint32_t w[4];
-                    load_words<16, NT>(base + (koff[k] & live), w);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) kw[u][k + i / 2][i % 2] = w[i];
-                }
-            }
-            if constexpr (DT == KV_I8)
-                ksc[u] = *(const f32x4u_t *)(c.k_scale + p.row[u] + 4 * cg);
-        }
-    };
-    auto load_values = [&](const TilePages<H> &p, int live) {
-#pragma unroll
-        for (int u = 0; u < H; ++u) {
-            const char *base = (const char *)c.v + p.row[u] * row_bytes;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int k = 0; k < NC; ++k)
-                    load_words<DC * ES, NT>(base + (voff[k] & live) + j * row_bytes,
-                                        vw[4 * u + j][k]);
-            if constexpr (DT == KV_I8)
-                vsc[u] = *(const f32x4u_t *)(c.v_scale + p.row[u] + 4 * cg);
-        }
-    };
-
-    float m = -INFINITY, l = 0.0f;
-    f32x4_t acc[NC * DC];
-    const f32x4_t zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int e = 0; e < NC * DC; ++e) acc[e] = zero4;
-
-    int t0 = first + kTile * wave;
-    if (t0 < last) {
-        TilePages<H> pg = find(t0);
-        load_keys(pg, -1);
-        load_values(pg, -1);
-        // queries: column x of the B operands, all blocks
-        Split<QK> qs[NB];
-        float sc = scale * 1.4426950408889634f;
-        {
-            float f[NB][8];
-            // heads past the block and dims past head_dim read others' and count as zero
-            const float *qp = q + (int64_t)b * q_stride + (int64_t)(hq0 + min(x, gn - 1)) * c.dim;
-#pragma unroll
-            for (int k = 0; k < NB; ++k) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int d = dim_of(k, half);
-                    const f32x4_t v = *(const f32x4u_t *)(qp + max(d, 0));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        f[k][4 * half + e] = x < gn && d >= 0 ? v[e] : 0.0f;
-                }
-            }
-            if constexpr (QK == kTwoHalf) {
-                float top = 0.0f;
-#pragma unroll
-                for (int k = 0; k < NB; ++k)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[k][e]));
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                // top in [2^(e-1), 2^e): to [2^14, 2^15); the shift undone in sc
-                const int up = top > 0.0f ? min(15 - ilogbf(top) - 1, 100) : 0;
-#pragma unroll
-                for (int k = 0; k < NB; ++k)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[k][e] = ldexpf(f[k][e], up);
-                sc = ldexpf(sc, -up);
-            }
-#pragma unroll
-            for (int k = 0; k < NB; ++k) qs[k].set(f[k]);
-        }
-        for (; t0 < last; t0 += kStep) {
-            // the next tile's loads go out as soon as this tile has used its own
-            const bool more = t0 + kStep < last;
-            const TilePages<H> next = find(more ? t0 + kStep : t0);
-            f32x4_t s[H];
-#pragma unroll
-            for (int u = 0; u < H; ++u) s[u] = zero4;
-#pragma unroll
-            for (int k = 0; k < NB; ++k)
+            auto find = [&](int t0) {
+                TilePages<H> p;
 #pragma unroll
                 for (int u = 0; u < H; ++u) {
-                    uint32_t a[8];
-                    if constexpr (DT == KV_I8) {
+                    // groups past the end read its page, and no entry past it
+                    const int t = t0 + 16 * u;
+                    const int page = tab[min(t, last - 1) >> c.shift];
+                    p.ok[u] = kv_page_ok(c, page);
+                    if (!p.ok[u]) set_status(d_status, W4_ERR_BAD_SHAPE);
+                    p.row[u] = kv_row(c, p.ok[u] ? page : 0, h, t & mask);
+                }
+                return p;
+            };
+
+            // `live` 0: every lane reads the group's first bytes (a load that nothing
+            // uses costs a cache line then, and no branch)
+            uint32_t kw[H][NB][KW];
+            uint32_t vw[NP][NC][VW];
+            f32x4_t ksc[H], vsc[H];
+            auto load_keys = [&](const TilePages<H> &p, int live) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            a[i] = codes_along(kw[u][k][i / 2] ^ 0x80808080u, i & 1);
-                    } else {
+                for (int u = 0; u < H; ++u) {
+                    const char *base = (const char *)c.k + p.row[u] * row_bytes;
 #pragma unroll
-                        for (int i = 0; i < KW; ++i) a[i] = kw[u][k][i];
+                    for (int k = 0; k < NB; ++k) {
+                        if (k >= 2 * PAIRS) {
+#pragma unroll
+                            for (int i = 0; i < KL; ++i)
+                                load_words<8 * ES / KL, NT>(base + (koff[k * KL + i] & live),
+                                                        kw[u][k] + i * KW / KL);
+                        } else if (k % 2 == 0) {
+                            uint32_t w[4];
+                            load_words<16, NT>(base + (koff[k] & live), w);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) kw[u][k + i / 2][i % 2] = w[i];
+                        }
+                    }
+                    if constexpr (DT == KV_I8)
+                        ksc[u] = *(const f32x4u_t *)(c.k_scale + p.row[u] + 4 * cg);
+                }
+            };
+            auto load_values = [&](const TilePages<H> &p, int live) {
+#pragma unroll
+                for (int u = 0; u < H; ++u) {
+                    const char *base = (const char *)c.v + p.row[u] * row_bytes;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int k = 0; k < NC; ++k)
+                            load_words<DC * ES, NT>(base + (voff[k] & live) + j * row_bytes,
+                                                vw[4 * u + j][k]);
+                    if constexpr (DT == KV_I8)
+                        vsc[u] = *(const f32x4u_t *)(c.v_scale + p.row[u] + 4 * cg);
+                }
+            };
+
+            float m = -INFINITY, l = 0.0f;
+            f32x4_t acc[NC * DC];
+            const f32x4_t zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int e = 0; e < NC * DC; ++e) acc[e] = zero4;
+
+            int t0 = first + kTile * wave;
+            if (t0 < last) {
+                TilePages<H> pg = find(t0);
+                load_keys(pg, -1);
+                load_values(pg, -1);
+                // queries: column x of the B operands, all blocks
+                Split<QK> qs[NB];
+                float sc = scale * 1.4426950408889634f;
+                {
+                    float f[NB][8];
+                    // heads past the block and dims past head_dim read others' and count as zero
+                    const float *qp =
+                        q + (int64_t)b * q_stride + (int64_t)(hq0 + min(x, gn - 1)) * c.dim;
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const int d = dim_of(k, half);
+                            const f32x4_t v = *(const f32x4u_t *)(qp + max(d, 0));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                f[k][4 * half + e] = x < gn && d >= 0 ? v[e] : 0.0f;
+                        }
+                    }
+                    if constexpr (QK == kTwoHalf) {
+                        float top = 0.0f;
+#pragma unroll
+                        for (int k = 0; k < NB; ++k)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[k][e]));
+                        top = fmaxf(top, __shfl_xor(top, 16));
+                        top = fmaxf(top, __shfl_xor(top, 32));
+                        // top in [2^(e-1), 2^e): to [2^14, 2^15); the shift undone in sc
+                        const int up = top > 0.0f ? min(15 - ilogbf(top) - 1, 100) : 0;
+#pragma unroll
+                        for (int k = 0; k < NB; ++k)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f[k][e] = ldexpf(f[k][e], up);
+                        sc = ldexpf(sc, -up);
                     }
 #pragma unroll
-                    for (int r = Split<QK>::terms - 1; r >= 0; --r)
-                        s[u] = mfma8<QK>(a, qs[k].w[r], s[u]);
+                    for (int k = 0; k < NB; ++k) qs[k].set(f[k]);
                 }
+                for (; t0 < last; t0 += kStep) {
+                    // the next tile's loads go out as soon as this tile has used its own
+                    const bool more = t0 + kStep < last;
+                    const TilePages<H> next = find(more ? t0 + kStep : t0);
+                    f32x4_t s[H];
 #pragma unroll
-            for (int u = 0; u < H; ++u)
+                    for (int u = 0; u < H; ++u) s[u] = zero4;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s[u][i] *= sc;
-                    if constexpr (DT == KV_I8) s[u][i] *= ksc[u][i];
-                }
-            load_keys(next, more ? -1 : 0);
-            bool whole = t0 >= lo && t0 + kTile <= last;
+                    for (int k = 0; k < NB; ++k)
 #pragma unroll
-            for (int u = 0; u < H; ++u) whole = whole && pg.ok[u];
-            // bit 4 u + i: this lane's position takes part
-            uint32_t in = (1u << NP) - 1;
-            if (!whole) {
+                        for (int u = 0; u < H; ++u) {
+                            uint32_t a[8];
+                            if constexpr (DT == KV_I8) {
 #pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const int t = t0 + 16 * (i / 4) + 4 * cg + i % 4;
-                    if (t < lo || t >= last || !pg.ok[i / 4]) {
-                        in &= ~(1u << i);
-                        s[i / 4][i % 4] = -INFINITY;
-                    }
-                }
-            }
-            if (parts.scores && x < gn) {
-                float *at = parts.scores +
-                            ((int64_t)b * q_heads + hq0 + x) * parts.score_stride + t0 + 4 * cg;
+                                for (int i = 0; i < 4; ++i)
+                                    a[i] = codes_along(kw[u][k][i / 2] ^ 0x80808080u, i & 1);
+                            } else {
 #pragma unroll
-                for (int u = 0; u < H; ++u) *(f32x4_t *)(at + 16 * u) = s[u];
-            }
-            float top = s[0][0];
-#pragma unroll
-            for (int i = 1; i < NP; ++i) top = fmaxf(top, s[i / 4][i % 4]);
-            if (__any(top > m)) {
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                top = fmaxf(top, m);
-                const float fade = top == -INFINITY ? 1.0f : pow2(m - top);
-                m = top;
-                l *= fade;
-                f32x4_t fr;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) fr[i] = __shfl(fade, 4 * cg + i);
-#pragma unroll
-                for (int e = 0; e < NC * DC; ++e)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[e][i] *= fr[i];
-            }
-            // nothing seen yet: every s is -infinity, and p is 0
-            const float ref = (m == -INFINITY ? 0.0f : m) - (PV == kTwoHalf ? 15.0f : 0.0f);
-            float p[NP];
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                p[i] = pow2(s[i / 4][i % 4] - ref);
-                l += p[i];
-            }
-            if constexpr (DT == KV_I8) {
-#pragma unroll
-                for (int i = 0; i < NP; ++i) p[i] *= vsc[i / 4][i % 4];
-                if (!whole) {
-#pragma unroll
-                    for (int i = 0; i < NP; ++i)
-                        if (!(in >> i & 1u)) p[i] = 0.0f;
-                }
-            } else if (!whole) {
-#pragma unroll
-                for (int j = 0; j < NP; ++j)
-#pragma unroll
-                    for (int k = 0; k < NC; ++k)
-#pragma unroll
-                        for (int i = 0; i < VW; ++i)
-                            if (!(in >> j & 1u)) vw[j][k][i] = 0;
-            }
-            {
-                Split<PV> ps;
-                ps.set(p);
-#pragma unroll
-                for (int k = 0; k < NC; ++k)
-#pragma unroll
-                    for (int e = 0; e < DC; ++e) {
-                        uint32_t v[8];
-                        if constexpr (DT == KV_F32) {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) v[j] = vw[j][k][e];
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t *v0 = vw[2 * j][k], *v1 = vw[2 * j + 1][k];
-                                if constexpr (DT == KV_I8)
-                                    v[j] = hi16_pair(fbits(code_at(v0[e / 4], e % 4)),
-                                                     fbits(code_at(v1[e / 4], e % 4)));
-                                else
-                                    v[j] = e % 2 ? hi16_pair(v0[e / 2], v1[e / 2])
-                                                 : lo16_pair(v0[e / 2], v1[e / 2]);
+                                for (int i = 0; i < KW; ++i) a[i] = kw[u][k][i];
                             }
+#pragma unroll
+                            for (int r = Split<QK>::terms - 1; r >= 0; --r)
+                                s[u] = mfma8<QK>(a, qs[k].w[r], s[u]);
                         }
 #pragma unroll
-                        for (int r = Split<PV>::terms - 1; r >= 0; --r)
-                            acc[k * DC + e] = mfma8<PV>(ps.w[r], v, acc[k * DC + e]);
+                    for (int u = 0; u < H; ++u)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            s[u][i] *= sc;
+                            if constexpr (DT == KV_I8) s[u][i] *= ksc[u][i];
+                        }
+                    load_keys(next, more ? -1 : 0);
+                    bool whole = t0 >= lo && t0 + kTile <= last;
+#pragma unroll
+                    for (int u = 0; u < H; ++u) whole = whole && pg.ok[u];
+                    // bit 4 u + i: this lane's position takes part
+                    uint32_t in = (1u << NP) - 1;
+                    if (!whole) {
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) {
+                            const int t = t0 + 16 * (i / 4) + 4 * cg + i % 4;
+                            if (t < lo || t >= last || !pg.ok[i / 4]) {
+                                in &= ~(1u << i);
+                                s[i / 4][i % 4] = -INFINITY;
+                            }
+                        }
                     }
+                    if (parts.scores && x < gn) {
+                        float *at = parts.scores +
+                                    ((int64_t)b * q_heads + hq0 + x) * parts.score_stride +
+                                    t0 + 4 * cg;
+#pragma unroll
+                        for (int u = 0; u < H; ++u) *(f32x4_t *)(at + 16 * u) = s[u];
+                    }
+                    float top = s[0][0];
+#pragma unroll
+                    for (int i = 1; i < NP; ++i) top = fmaxf(top, s[i / 4][i % 4]);
+                    if (__any(top > m)) {
+                        top = fmaxf(top, __shfl_xor(top, 16));
+                        top = fmaxf(top, __shfl_xor(top, 32));
+                        top = fmaxf(top, m);
+                        const float fade = top == -INFINITY ? 1.0f : pow2(m - top);
+                        m = top;
+                        l *= fade;
+                        f32x4_t fr;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) fr[i] = __shfl(fade, 4 * cg + i);
+#pragma unroll
+                        for (int e = 0; e < NC * DC; ++e)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[e][i] *= fr[i];
+                    }
+                    // nothing seen yet: every s is -infinity, and p is 0
+                    const float ref = (m == -INFINITY ? 0.0f : m) - (PV == kTwoHalf ? 15.0f : 0.0f);
+                    float p[NP];
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        p[i] = pow2(s[i / 4][i % 4] - ref);
+                        l += p[i];
+                    }
+                    if constexpr (DT == KV_I8) {
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) p[i] *= vsc[i / 4][i % 4];
+                        if (!whole) {
+#pragma unroll
+                            for (int i = 0; i < NP; ++i)
+                                if (!(in >> i & 1u)) p[i] = 0.0f;
+                        }
+                    } else if (!whole) {
+#pragma unroll
+                        for (int j = 0; j < NP; ++j)
+#pragma unroll
+                            for (int k = 0; k < NC; ++k)
+#pragma unroll
+                                for (int i = 0; i < VW; ++i)
+                                    if (!(in >> j & 1u)) vw[j][k][i] = 0;
+                    }
+                    {
+                        Split<PV> ps;
+                        ps.set(p);
+#pragma unroll
+                        for (int k = 0; k < NC; ++k)
+#pragma unroll
+                            for (int e = 0; e < DC; ++e) {
+                                uint32_t v[8];
+                                if constexpr (DT == KV_F32) {
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) v[j] = vw[j][k][e];
+                                } else {
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) {
+                                        const uint32_t *v0 = vw[2 * j][k], *v1 = vw[2 * j + 1][k];
+                                        if constexpr (DT == KV_I8)
+                                            v[j] = hi16_pair(fbits(code_at(v0[e / 4], e % 4)),
+                                                             fbits(code_at(v1[e / 4], e % 4)));
+                                        else
+                                            v[j] = e % 2 ? hi16_pair(v0[e / 2], v1[e / 2])
+                                                         : lo16_pair(v0[e / 2], v1[e / 2]);
+                                    }
+                                }
+#pragma unroll
+                                for (int r = Split<PV>::terms - 1; r >= 0; --r)
+                                    acc[k * DC + e] = mfma8<PV>(ps.w[r], v, acc[k * DC + e]);
+                            }
+                    }
+                    load_values(next, more ? -1 : 0);
+                    pg = next;
+                }
             }
-            load_values(next, more ? -1 : 0);
-            pg = next;
-        }
-    }
 
-    // the four waves' parts, added in wave order
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    if (cg == 0) s_m[wave][x] = m, s_l[wave][x] = l;
+            // the four waves' parts, added in wave order
+            l += __shfl_xor(l, 16);
+            l += __shfl_xor(l, 32);
+            if (cg == 0) s_m[wave][x] = m, s_l[wave][x] = l;
 #pragma unroll
-    for (int k = 0; k < NC; ++k)
+            for (int k = 0; k < NC; ++k)
 #pragma unroll
-        for (int e = 0; e < DC; ++e)
+                for (int e = 0; e < DC; ++e)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                s_acc[wave][4 * cg + i][(16 * k + x) * DC + e] = acc[k * DC + e][i];
-    __syncthreads();
-    const int64_t row = (int64_t)b * q_heads + hq0;
-    const int64_t slot = (2 * (int64_t)blockIdx.x + (from == 0)) * 16;
-    for (int i = threadIdx.x; i < gn * c.dim; i += 64 * kWaves) {
-        const int g = i / c.dim, d = i % c.dim;
-        float M = s_m[0][g];
+                    for (int i = 0; i < 4; ++i)
+                        s_acc[wave][4 * cg + i][(16 * k + x) * DC + e] = acc[k * DC + e][i];
+            __syncthreads();
+            const int64_t row = (int64_t)b * q_heads + hq0;
+            const int64_t slot = (2 * (int64_t)blockIdx.x + (from == 0)) * 16;
+            for (int i = threadIdx.x; i < gn * c.dim; i += 64 * kWaves) {
+                const int g = i / c.dim, d = i % c.dim;
+                float M = s_m[0][g];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) M = fmaxf(M, s_m[w][g]);
-        float L = 0.0f, o = 0.0f;
+                for (int w = 1; w < kWaves; ++w) M = fmaxf(M, s_m[w][g]);
+                float L = 0.0f, o = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            const float f = s_m[w][g] == -INFINITY ? 0.0f : pow2(s_m[w][g] - M);
-            L += f * s_l[w][g];
-            o += f * s_acc[w][g][d];
+                for (int w = 0; w < kWaves; ++w) {
+                    const float f = s_m[w][g] == -INFINITY ? 0.0f : pow2(s_m[w][g] - M);
+                    L += f * s_l[w][g];
+                    o += f * s_acc[w][g][d];
+                }
+                if (whole_block) {
+                    out[(row + g) * c.dim + d] = L == 0.0f ? 0.0f : o / L;
+                    if (parts.whole && d == 0) parts.whole[row + g] = make_float2(M, L);
+                } else {
+                    parts.sum[(slot + g) * c.dim + d] = o;
+                    if (d == 0) parts.stat[slot + g] = make_float2(M, L);
+                }
+            }
+            __syncthreads();
+        } else if (steps == 0 && u == start) {
+            // nothing to attend to
+            for (int i = threadIdx.x; i < gn * c.dim; i += 64 * kWaves)
+                out[((int64_t)b * q_heads + hq0) * c.dim + i] = 0.0f;
         }
-        if (whole_block) {
-            out[(row + g) * c.dim + d] = L == 0.0f ? 0.0f : o / L;
-            if (parts.whole && d == 0) parts.whole[row + g] = make_float2(M, L);
-        } else {
-            parts.sum[(slot + g) * c.dim + d] = o;
-            if (d == 0) parts.stat[slot + g] = make_float2(M, L);
+        u = stop;
+        if (u < u1 && vb + 1 == blocks) {
+            base = u;
+            ++b;
+            n = kv_length(lens, b, most, d_status), lo = first_of(b), steps = kv_steps(lo, n);
         }
-    }
-    __syncthreads();
-    } else if (steps == 0 && u == start) {
-        // nothing to attend to
-        for (int i = threadIdx.x; i < gn * c.dim; i += 64 * kWaves)
-            out[((int64_t)b * q_heads + hq0) * c.dim + i] = 0.0f;
-    }
-    u = stop;
-    if (u < u1 && vb + 1 == blocks) {
-        base = u;
-        ++b;
-        n = kv_length(lens, b, most, d_status), lo = first_of(b), steps = kv_steps(lo, n);
-    }
     }
 }
 

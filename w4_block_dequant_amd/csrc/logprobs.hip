@@ -31,6 +31,10 @@
 // NaN or +infinity makes S NaN (x - m = infinity - infinity), and nothing else
 // does: a -infinity gives e = 0, and in W a difference below -1e30 counts as
 // -1e30, whose e is 0.
+//
+// Measured: 2048 x 100003 top 20 138 us, 5.9 TB/s (without a list 126, 6.5); 58 x 50257
+// top 5 14.2 us (two launches, sorting and joining), top 1 9.6; one row of 50257
+// top 1 8.4-8.9 us in one launch.
 #include <math.h>
 
 #include "kv.h"
