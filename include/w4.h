@@ -441,7 +441,8 @@ int kv_append(const kv_cache *cache, const float *k, int64_t k_stride, const flo
  * below 2^31 (W4_ERR_BAD_SHAPE otherwise).  The
  * workspace (kv_attend_workspace_bytes, 256-byte aligned, any contents, not
  * shared with a call in flight on another stream) holds the parts that the
- * length is split into.                                                    */
+ * length is split into; its size is asked for with the bound in force, the
+ * smaller of max_len (unless 0) and cols * page_size.                      */
 size_t kv_attend_workspace_bytes(const kv_cache *cache, int64_t seqs, int64_t q_heads,
                                  int64_t max_len);
 

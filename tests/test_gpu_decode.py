@@ -309,6 +309,71 @@ def test_attend_on_another_stream_and_in_a_graph():
         assert torch.equal(out, ref) and torch.equal(w, w2)
 
 
+@pytest.mark.parametrize("dtype", ["int8", "bf16"])
+def test_attend_and_append_with_arrays_off_16_bytes(dtype):
+    """Scales, weights, lengths and the table need 4-byte alignment only."""
+    note(f"attend off alignment {dtype}")
+    c = Cache(dtype, [300, 45], 2, 40, 16, 41, weight=True)
+    (K, V, ks, vs, w), table = c.on_gpu()
+    q = torch.randn((2, 4, 40), generator=torch.Generator().manual_seed(42)).to(DEV)
+    lens = torch.tensor(c.lens, dtype=torch.int32, device=DEV)
+
+    def shifted(t):
+        if t is None:
+            return None
+        wide = torch.zeros(t.numel() + 1, dtype=t.dtype, device=DEV)
+        wide[1:] = t.reshape(-1)
+        return wide[1:].view(t.shape)
+
+    w1, w2 = w.clone(), shifted(w)
+    ref = w4.kv_attend(q, K, V, table, lens, k_scale=ks, v_scale=vs, weight=w1)
+    got = w4.kv_attend(shifted(q), K, V, shifted(table), shifted(lens), k_scale=shifted(ks),
+                       v_scale=shifted(vs), weight=w2, out=shifted(torch.zeros_like(ref)))
+    assert torch.equal(ref, got) and torch.equal(w1, w2)
+    x = torch.randn((2, 2, 40), generator=torch.Generator().manual_seed(43)).to(DEV)
+    seq = torch.tensor([1, 0], dtype=torch.int32, device=DEV)
+    at = torch.tensor([44, 7], dtype=torch.int32, device=DEV)
+    K2, V2, ks2, vs2 = K.clone(), V.clone(), shifted(ks), shifted(vs)
+    w4.kv_append(x, x, K, V, table, seq, at, k_scale=ks, v_scale=vs, weight=w1)
+    w4.kv_append(shifted(x), shifted(x), K2, V2, shifted(table), shifted(seq), shifted(at),
+                 k_scale=ks2, v_scale=vs2, weight=w2)
+    assert torch.equal(bits(K), bits(K2)) and torch.equal(bits(V), bits(V2))
+    assert torch.equal(w1, w2)
+    if ks is not None:
+        assert torch.equal(bits(ks), bits(ks2)) and torch.equal(bits(vs), bits(vs2))
+
+
+def test_append_and_evict_in_a_graph():
+    """Captured once, replayed on new rows, places, lengths and weights."""
+    note("append and evict graph")
+    c = Cache("bf16", [90, 40], 2, 64, 16, 44, weight=True, spare=8)
+    (K, V, _, _, w), table = c.on_gpu()
+    x = torch.randn((2, 2, 64), device=DEV)
+    seq = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    at = torch.tensor([89, 39], dtype=torch.int32, device=DEV)
+    lens = torch.tensor(c.lens, dtype=torch.int32, device=DEV)
+    out = torch.tensor(c.free[:6].reshape(2, 3).astype(np.int32), device=DEV)
+    kept = torch.empty((2, 2, 48), dtype=torch.int32, device=DEV)
+    new = torch.empty(2, dtype=torch.int32, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w4.kv_append(x, x, K, V, table, seq, at, weight=w)
+        w4.kv_evict(K, V, w, table, lens, 48, 5, out, kept=kept, lens_out=new)
+    g = torch.Generator(device=DEV).manual_seed(45)
+    for n in (90, 33, 64, 0):
+        x.normal_(generator=g)
+        w.uniform_(generator=g)
+        lens[0] = n
+        at[0] = max(n - 1, 0)
+        K2, V2, w2 = K.clone(), V.clone(), w.clone()
+        graph.replay()
+        w4.kv_append(x, x, K2, V2, table, seq, at, weight=w2)
+        kept2, new2 = w4.kv_evict(K2, V2, w2, table, lens, 48, 5, out)
+        assert torch.equal(kept, kept2) and torch.equal(new, new2)
+        assert torch.equal(bits(K), bits(K2)) and torch.equal(bits(V), bits(V2))
+        assert torch.equal(bits(w), bits(w2))
+
+
 # ---- append --------------------------------------------------------------------
 def stored(x, dtype):
     if dtype != "int8":

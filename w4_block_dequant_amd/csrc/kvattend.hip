@@ -179,6 +179,11 @@ __device__ __forceinline__ f32x4_t mfma8(const uint32_t *a, const uint32_t *b, f
 template <int DT>
 constexpr int kElem = DT == KV_F32 ? 4 : DT == KV_I8 ? 1 : 2;
 
+// Words of four-byte alignment: int8 rows of an odd number of 8 bytes leave 16 of
+// them on an 8-byte boundary.
+typedef uint32_t u32x2u_t __attribute__((ext_vector_type(2), aligned(4)));
+typedef uint32_t u32x4u_t __attribute__((ext_vector_type(4), aligned(4)));
+
 // BYTES from p, as words.  NT: read once, not to be kept in the caches.
 template <bool NT, class T>
 __device__ __forceinline__ T load_as(const char *p) {
@@ -189,13 +194,13 @@ __device__ __forceinline__ void load_words(const char *p, uint32_t *w) {
     if constexpr (BYTES == 4) {
         w[0] = load_as<NT, uint32_t>(p);
     } else if constexpr (BYTES == 8) {
-        const u32x2_t v = load_as<NT, u32x2_t>(p);
+        const u32x2_t v = load_as<NT, u32x2u_t>(p);
         w[0] = v.x;
         w[1] = v.y;
     } else {
 #pragma unroll
         for (int i = 0; i < BYTES / 16; ++i) {
-            const u32x4_t v = load_as<NT, u32x4_t>(p + 16 * i);
+            const u32x4_t v = load_as<NT, u32x4u_t>(p + 16 * i);
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
         }

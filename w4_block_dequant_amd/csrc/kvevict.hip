@@ -181,7 +181,10 @@ __global__ __launch_bounds__(kSelThreads) void k_kv_select(
         const uint64_t up = __ballot(in && key > least), eq = __ballot(in && key == least);
         const uint32_t rank = below(eq, tied);  // among the equal ones
         const uint32_t place = below(up, base) + min(rank, ties);
-        if (in && (key > least || (key == least && rank < ties))) to[place] = t;
+        // (place < want unless the weights change under the call, which is the
+        // caller's race, but not a write out of place)
+        if (in && (key > least || (key == least && rank < ties)) && place < (uint32_t)want)
+            to[place] = t;
         base += (uint32_t)__popcll(up);
         tied += (uint32_t)__popcll(eq);
     });
