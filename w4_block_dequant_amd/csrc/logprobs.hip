@@ -14,13 +14,14 @@
 // larger value or, of equal ones, the lower index.  Each wave holds its 64
 // largest keys in descending order, one in a lane, and a queue of new ones.  A
 // logit is looked at again only if its lane's largest of 16 reaches the
-// threshold, a key that at least `top` keys of the row reach: at first the
-// top-th largest of the wave's lane maxima, later the top-th key of the list
-// or, if that is larger, any other wave's.  Keys past the threshold enter the
+// threshold, a key that at least `top` keys of the row reach: before
+// the first logits are counted, the smallest over the waves of each wave's
+// ceil(top / waves)-th largest lane maximum, later also the top-th key of any
+// wave's list.  Keys past the threshold enter the
 // queue; at 64 they are sorted and merged into the list.  Of logits drawn alike
-// few ever do: if no queue filled up, the keys of all queues that pass the last
-// threshold are sorted at once where they are at most 64; otherwise the waves'
-// lists are merged two by two.  Which keys get so far depends on the waves'
+// few ever do: if no queue filled up, the keys of all queues that pass the
+// threshold of the whole row's lane maxima are sorted at once where they are at
+// most 64; otherwise the waves' lists are merged two by two.  Which keys get so far depends on the waves'
 // timing, the `top` largest do not.  For the largest entry alone a
 // lane keeps its own best key and the keys are compared at the end.
 //
@@ -32,9 +33,9 @@
 // does: a -infinity gives e = 0, and in W a difference below -1e30 counts as
 // -1e30, whose e is 0.
 //
-// Measured: 2048 x 100003 top 20 138 us, 5.9 TB/s (without a list 126, 6.5); 58 x 50257
-// top 5 14.2 us (two launches, sorting and joining), top 1 9.6; one row of 50257
-// top 1 8.4-8.9 us in one launch.
+// Measured: 2048 x 100003 top 20 137 us, 6.0 TB/s (top 64 147, without a list 126, 6.5);
+// 512 x 50257 top 20 26 us, top 1 21; 58 x 50257 top 5 13.9 us (two launches, sorting and
+// joining), top 1 9.6; one row of 50257 top 1 8.4-8.9 us in one launch.
 #include <math.h>
 
 #include "kv.h"
@@ -229,7 +230,8 @@ enum LpMode { kNone, kOne, kList };
 __device__ __forceinline__ uint64_t key_of(float v, uint32_t n) {
     return (uint64_t)order_key(v) << 32 | (uint32_t)~n;
 }
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+template <class K>
+__device__ __forceinline__ K wave_max(K v) {
     v = max(v, lane_xor<1>(v));
     v = max(v, lane_xor<2>(v));
     v = max(v, lane_xor<4>(v));
@@ -247,6 +249,7 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restr
                                                             float4 *sums, uint64_t *keys) {
     __shared__ uint64_t s_key[kLpWaves][128];  // queues, later lists
     __shared__ uint64_t s_limit, s_last[64];
+    __shared__ uint32_t s_peak[2][kLpWaves];
     __shared__ int s_flushed, s_count;
     __shared__ LpSums s_sum[kLpWaves];
     const int64_t row = blockIdx.x / chunks;
@@ -259,16 +262,13 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restr
     const uint32_t end = min(begin + (uint32_t)chunk, (uint32_t)N);
     LpToken token;
     if (chunks == 1 && wave == 0) token = lp_token(o, row, x, N);
-    if (MODE == kList) {
-        if (threadIdx.x == 0) s_limit = 0, s_flushed = 0, s_count = 0;
-        __syncthreads();
-    }
+    if (MODE == kList && threadIdx.x == 0) s_limit = 0, s_flushed = 0, s_count = 0;
 
     LpSums r = {-INFINITY, 0.0f, 0.0f};
     uint64_t list = 0, limit = 0;  // descending keys; the threshold (0: none yet)
     float reach = -INFINITY;       // its value
     int queued = 0;
-    bool fresh = true;
+    uint32_t round = 0;
     auto raise = [&](uint64_t to) {
         if (to > limit) {
             limit = to;
@@ -292,6 +292,25 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restr
     };
 
     constexpr int kSpan = 256 * kLpLoads;  // logits of a wave at a time
+    // A value that `top` logits of the row reach, from the lane maxima of the waves
+    // that have a whole span: each has `rank` lanes that reach its own.
+    const int active = (int)min(max((end - begin) / kSpan, 1u), (uint32_t)kLpWaves);
+    const int rank = (top + active - 1) / active;
+    auto reached = [&](float lane_max, uint32_t *peaks) {
+        uint32_t key = order_key(lane_max);
+        if (rank == 1) {
+            key = wave_max(key);
+        } else {
+            sort64(key);
+            key = (uint32_t)__builtin_amdgcn_readlane((int)key, rank - 1);
+        }
+        if (lane == 0) peaks[wave] = wave < active ? key : 0xFFFFFFFFu;
+        __syncthreads();
+        uint32_t least = peaks[0];
+#pragma unroll
+        for (int w = 1; w < kLpWaves; ++w) least = min(least, peaks[w]);
+        return (uint64_t)least << 32;
+    };
     f32x4_t next[kLpLoads];
     auto load = [&](uint32_t at) {
         // a lane's load j is logits at + 256 j + 4 lane ..; past the end: -infinity
@@ -309,6 +328,14 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restr
     };
     uint32_t at = begin + wave * kSpan;
     if (at < end) load(at);
+    if constexpr (MODE == kList) {
+        float peak = -INFINITY;
+        if (at < end) {
+#pragma unroll
+            for (int j = 0; j < 4 * kLpLoads; ++j) peak = fmaxf(peak, next[j / 4][j % 4]);
+        }
+        raise(reached(peak, s_peak[0]));
+    }
     for (; at < end; at += kLpWaves * kSpan) {
         f32x4_t v[kLpLoads];
 #pragma unroll
@@ -334,7 +361,7 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restr
         }
         if constexpr (MODE == kOne) {
             // equal values keep the lower index, which came first
-            if (fresh || best > reach) {
+            if (round == 0 || best > reach) {
                 reach = best;
                 uint32_t j = 0;
 #pragma unroll
@@ -342,18 +369,9 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restr
                     if (v[i / 4][i % 4] == best) j = 256 * (i / 4) + i % 4;
                 list = key_of(best, at + 4 * lane + j);
             }
-            fresh = false;
+            round = 1;
         }
         if constexpr (MODE == kList) {
-            if (fresh) {
-                uint32_t first = order_key(best);
-                sort64(first);
-                const uint64_t to =
-                    (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)first, top - 1) << 32;
-                if (lane == 0) atomicMax((unsigned long long *)&s_limit, (unsigned long long)to);
-                raise(to);
-                fresh = false;
-            }
             raise(*(volatile uint64_t *)&s_limit);
             if (__any(best >= reach)) {
                 uint32_t bits = 0;  // of a lane's 16 that may pass
@@ -386,6 +404,7 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restr
             }
         }
     }
+    const float lane_max = r.m;
     r = lp_wave(r);
     if (lane == 0) s_sum[wave] = r;
     if constexpr (MODE == kOne) {
@@ -393,18 +412,18 @@ __global__ __launch_bounds__(64 * kLpWaves) void k_logprobs(const float *__restr
         if (lane == 0) s_key[wave][0] = list;
     }
     if constexpr (MODE == kList) {
-        __syncthreads();
+        raise(reached(lane_max, s_peak[1]));
         const bool sparse = s_flushed == 0;
         if (sparse) {
             // without a flush the threshold is a value: all its keys are larger
             const uint64_t k = lane < queued ? s_key[wave][lane] : 0;
-            const uint64_t mask = __ballot(k > s_limit);
+            const uint64_t mask = __ballot(k > limit);
             int at = 0;
             if (lane == 0) at = atomicAdd(&s_count, (int)__popcll(mask));
             at = __builtin_amdgcn_readfirstlane(at) +
                  (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
                                                 __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-            if (k > s_limit && at < 64) s_last[at] = k;
+            if (k > limit && at < 64) s_last[at] = k;
         }
         __syncthreads();
         if (sparse && s_count <= 64) {
