@@ -714,7 +714,8 @@ def kv_attend(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, table: torch.Te
 
     scale: 1 / sqrt(head_dim) by default.  max_len: a bound on lens that the host knows (0: what
     the table holds); it sets how the length is split.  weight: if given, grows by the attention
-    that each position takes."""
+    that each position takes; the workspace then holds q_heads * max_len scores for each
+    sequence, so a bound keeps it small."""
     cache = _kv_cache(K, V, k_scale, v_scale, weight)
     seqs, q_heads, qs = _kv_rows(q, "q", cache.head_dim)
     _, cols = _kv_table(table, "table", seqs)

@@ -494,16 +494,17 @@ LogprobsPlan plan_logprobs(int64_t M, int64_t N, int64_t top) {
     LogprobsPlan p;
     p.chunk = N;
     if (M <= 0) return p;
-    // Two workgroups for each compute unit, none with less than 16384 logits, or
-    // 4096 if it has a list to sort (one row of 50257, top 5, pieces of 2048:
-    // 12.6 us, of 4096: 11.7).  One workgroup streams 65536 logits in less time
-    // than a second launch adds, without a list (one row of 50257, top 1: 8.3 us,
-    // in pieces and joined 7.7 but a launch of the host more; 58 rows 9.6 against
-    // 11.0; one row of 100003 12.6 against 10.1).
-    constexpr int64_t kWgs = 512;
-    const int64_t least = top > 1 ? 4096 : 16384;
+    // One workgroup for each compute unit, none with less than 16384 logits (top
+    // 20, pieces of 4096 / 8192 / 16384 / 32768: one row of 50257 11.8 / 12.1 /
+    // 12.8 / 13.4 us, 58 rows 16.7 / 17.2 / 15.9 / 17.7, 100 of 30000 16.3 / 17.2 /
+    // 14.1 / 14.0, 20 of 160000 18.9 / 18.8 / 16.9 / 19.1; 150 of 50257 in three
+    // pieces 20.1, whole 18.7).  Without a list one workgroup streams 65536 logits
+    // in less time than a second launch adds (58 rows of 50257, top 1: 9.6 us,
+    // joined 11.0; one row 8.4 against 7.7, but a launch of the host less; one of
+    // 100003 12.6 against 10.1).
+    constexpr int64_t kWgs = 256, kLeast = 16384;
     int64_t chunks = kWgs / M;
-    if (chunks > N / least) chunks = N / least;
+    if (chunks > N / kLeast) chunks = N / kLeast;
     if (top <= 1 && N <= 65536) chunks = 1;
     if (chunks <= 1) return p;
     p.chunk = (int64_t)align_up((size_t)cdiv(N, chunks), 256);
