@@ -678,12 +678,14 @@ __device__ __forceinline__ int64_t part_slot(int w0, int i) {
 __device__ __forceinline__ void joined(const float2 *stat, int w0, int count, int g, float &M,
                                        float &L) {
     const int lane = threadIdx.x & 63;
-    M = -INFINITY;
-    for (int i = lane; i < count; i += 64) M = fmaxf(M, stat[part_slot(w0, i) + g].x);
+    const float2 none = make_float2(-INFINITY, 0.0f);
+    const float2 mine = lane < count ? stat[part_slot(w0, lane) + g] : none;
+    M = mine.x;
+    for (int i = lane + 64; i < count; i += 64) M = fmaxf(M, stat[part_slot(w0, i) + g].x);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
-    L = 0.0f;
-    for (int i = lane; i < count; i += 64) {
+    L = mine.y != 0.0f ? pow2(mine.x - M) * mine.y : 0.0f;
+    for (int i = lane + 64; i < count; i += 64) {
         const float2 v = stat[part_slot(w0, i) + g];
         if (v.y != 0.0f) L += pow2(v.x - M) * v.y;
     }
@@ -714,15 +716,22 @@ __global__ __launch_bounds__(256) void k_kv_join(const int32_t *__restrict__ tab
         const int2 own = parts.owner[(b * c.heads + h) * gblocks + g / 16];
         if (own.x == own.y) return;  // one workgroup had it whole (or it is empty)
         const int count = own.y - own.x + 1;
-        float M, L;
-        joined(parts.stat, own.x, count, g % 16, M, L);
         const int quad = threadIdx.x & ((1 << quad_bits) - 1), group = threadIdx.x >> quad_bits;
         const int groups = 256 >> quad_bits, d = min(4 * quad, c.dim - 4);
-        f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+        // the first part of a group is on its way while the statistics are joined
+        // (a group without one reads the last part's)
+        f32x4_t v, o = {0.0f, 0.0f, 0.0f, 0.0f};
+        float2 st;
+        auto load = [&](int i) {
+            const int64_t slot = part_slot(own.x, min(i, count - 1)) + g % 16;
+            v = *(const f32x4_t *)(parts.sum + slot * c.dim + d);
+            st = parts.stat[slot];
+        };
+        load(group);
+        float M, L;
+        joined(parts.stat, own.x, count, g % 16, M, L);
         for (int i = group; i < count; i += groups) {
-            const int64_t slot = part_slot(own.x, i) + g % 16;
-            const f32x4_t v = *(const f32x4_t *)(parts.sum + slot * c.dim + d);
-            const float2 st = parts.stat[slot];
+            if (i > group) load(i);
             const float f = st.y != 0.0f ? pow2(st.x - M) : 0.0f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[j] = fmaf(f, v[j], o[j]);
