@@ -63,7 +63,7 @@
 // 16 x 4096 of 32 heads: bf16 of 128 163 us, 6.6 TB/s; fp32 of 128 317 us, 6.8; int8 of
 // 128 92 us, 6.0, of 96 79 us, 5.3 (96-byte rows straddle lines); ragged batches of
 // 180-210 MB 3.5-4.1 TB/s (5 us of start, 4 of joining); one sequence of 4095 of
-// 32 x 96 bf16 17.2 us, 2.9 TB/s; 59 positions of 12 x 64 fp32 6.6 us, one launch
+// 32 x 96 bf16 16.8 us, 3.0 TB/s; 59 positions of 12 x 64 fp32 6.6 us, one launch
 // and a chain of loads (length, page, key).
 #include <math.h>
 
@@ -313,7 +313,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_kv_attend(
         const uint32_t each = total / groups, rest = total % groups;
         u0 = (int)(blockIdx.x * each + blockIdx.x * rest / groups);
         u1 = (int)((blockIdx.x + 1) * each + (blockIdx.x + 1) * rest / groups);
-        for (int i0 = 0;; i0 += 64) {
+        // (found before the list ends, unless the lengths change under the call)
+        for (int i0 = 0; i0 < seqs; i0 += 64) {
             const int st = i0 == 0 ? mine : steps_of(i0 + lane);
             const int have = i0 + lane < seqs ? kv_units(st, part) * blocks : 0;
             const int upto = wave_scan(have);
